@@ -338,6 +338,131 @@ HS2_API hs2_status hs2_bridge_kv_proj(const hs2_bf16* Hs, int T, int hidden, con
                               hs2_bf16* KV, void* workspace, size_t workspace_bytes, hs2_stream stream);
 
 /* ---------------------------------------------------------------------------------
+ * Query and key heads before the attention: norm and position rotation
+ * ---------------------------------------------------------------------------------
+ * The calls above take Q and K as they enter the product. These make them from a projection's rows:
+ * every head's row x (d elements) of the token at position t becomes
+ *   n = x * rsqrt(mean(x^2) + eps) * weight            (weights NULL: n = x)
+ *   (a, b) -> mscale * (a cos - b sin, b cos + a sin)  for each pair i of the first `rot` elements,
+ * the angle positions[t] * inv_freq[i], computed in 64 bits; pair i is (i, i + rot / 2), or with
+ * interleaved != 0 (2 i, 2 i + 1). Elements from rot on are not rotated. 32-bit arithmetic, one
+ * rounding at the end.
+ * Q    rows of T tokens, Hq heads each: element e of head h of token t at Q[t * q_token_stride +
+ *      h * q_head_stride + e] (strides in elements, multiples of 8, e.g. those of a fused projection's
+ *      rows); K the same with Hk heads (Hk == 0, K == NULL: a layer that reuses another's cache has
+ *      queries only)
+ * positions [T] int32, inv_freq [rot / 2] fp64 (radians per position): DEVICE
+ * q_weight, k_weight [d] bf16, or fp32 with weight_fp32 != 0: both (k_weight only with Hk > 0) or neither
+ * q_out [T, Hq, d], k_out [T, Hk, d] bf16, contiguous
+ * Supported: d in {64, 128}, rot % 16 == 0, 16 <= rot <= d; T == 0 does nothing. No workspace.
+ */
+HS2_API hs2_status hs2_qk_norm_rope(const hs2_bf16* Q, const hs2_bf16* K, long long q_token_stride,
+                                    long long q_head_stride, long long k_token_stride, long long k_head_stride,
+                                    const int32_t* positions, const double* inv_freq, int T, int Hq, int Hk, int d,
+                                    int rot, int interleaved, float mscale, float eps, const void* q_weight,
+                                    const void* k_weight, int weight_fp32, hs2_bf16* q_out, hs2_bf16* k_out,
+                                    hs2_stream stream);
+
+/* Its backward pass. With g the upstream gradient rotated back (the transpose, times mscale), u = g * weight
+ * and r = rsqrt(mean(x^2) + eps):  dx = r * (u - x r^2 mean(u x)),  dweight = sum over rows of g * x * r.
+ * Q, K, positions, inv_freq and the weights as in the forward call (without weights Q and K are not read)
+ * dq_out [T, Hq, d] bf16, dk_out [T, Hk, d] bf16, or fp32 with dk_out_fp32 != 0 (what the attention's
+ *      backward accumulates): contiguous
+ * dQ, dK [T, H, d] bf16, contiguous (written); dq_weight, dk_weight [d] fp32 (written; only with weights)
+ * The weights' gradients are summed in a fixed order (they do not vary from run to run).
+ */
+HS2_API size_t hs2_qk_norm_rope_bwd_workspace_bytes(int T, int Hq, int Hk, int d);
+HS2_API hs2_status hs2_qk_norm_rope_bwd(const hs2_bf16* Q, const hs2_bf16* K, long long q_token_stride,
+                                        long long q_head_stride, long long k_token_stride, long long k_head_stride,
+                                        const int32_t* positions, const double* inv_freq, int T, int Hq, int Hk, int d,
+                                        int rot, int interleaved, float mscale, float eps, const void* q_weight,
+                                        const void* k_weight, int weight_fp32, const hs2_bf16* dq_out,
+                                        const void* dk_out, int dk_out_fp32, hs2_bf16* dQ, hs2_bf16* dK,
+                                        float* dq_weight, float* dk_weight, void* workspace, size_t workspace_bytes,
+                                        hs2_stream stream);
+
+/* The serving form: the same pass writes the rotated keys and the values (V, strides as Q's) into a paged
+ * cache, row slots[t] (page slots[t] / page_size, row slots[t] % page_size) of every key head.
+ * slots [T] int32 (DEVICE): distinct; a negative slot marks a padding row, of which nothing is read or
+ *      written (its row of q_out stays as it was); one past the pool is recorded as HS2_ERR_DEVICE_BOUNDS
+ *      and its cache rows are skipped (its queries are written)
+ * k_pages, v_pages  pools of n_pages pages: element e of head h of row r of page g at [g * strides[0] +
+ *      r * strides[1] + h * strides[2] + e] (k_page_strides, v_page_strides: HOST arrays of 3, in
+ *      elements, positive multiples of 16 bytes); bf16, or with e4m3 != 0 codes of K / k_scale and
+ *      V / v_scale (rounded once to nearest even, saturating at 448)
+ * Workspace: hs2_qk_norm_rope_paged_workspace_bytes (the status block).
+ */
+HS2_API size_t hs2_qk_norm_rope_paged_workspace_bytes(void);
+HS2_API hs2_status hs2_qk_norm_rope_paged(const hs2_bf16* Q, const hs2_bf16* K, const hs2_bf16* V,
+                                          long long q_token_stride, long long q_head_stride, long long k_token_stride,
+                                          long long k_head_stride, long long v_token_stride, long long v_head_stride,
+                                          const int32_t* positions, const int32_t* slots, const double* inv_freq, int T,
+                                          int Hq, int Hk, int d, int rot, int interleaved, float mscale, float eps,
+                                          const void* q_weight, const void* k_weight, int weight_fp32, hs2_bf16* q_out,
+                                          void* k_pages, void* v_pages, const long long* k_page_strides,
+                                          const long long* v_page_strides, int n_pages, int page_size, int e4m3,
+                                          float k_scale, float v_scale, void* workspace, size_t workspace_bytes,
+                                          hs2_stream stream);
+
+/* ---------------------------------------------------------------------------------
+ * Page tables from the requests' lengths
+ * ---------------------------------------------------------------------------------
+ * One serving step's bookkeeping on the device: request b holds lens[b] cached tokens in its first
+ * ceil(lens[b] / page_size) page-table entries and gains delta[b] tokens (negative: its cache is cut
+ * back; -lens[b]: it ends).
+ * page_table [B, max_pages] int32 (updated): the entries of the pages gained are written; entries past
+ *      a request's last page are not read and not cleared
+ * free_ring [ring_size] int32 (updated), free_state [2] int32 {head, count}: the free pages are
+ *      free_ring[(head + i) % ring_size], i < count; ring_size at least the pool's number of pages.
+ *      Pages gained are taken from the head in request order, pages given back are appended behind the
+ *      tail (they serve the next call, not this one)
+ * lens_out [B], free_state_out [2] int32: the values after the step (they may be lens and free_state)
+ * cu_tokens [B + 1] int32: the new tokens of request b are the packed rows cu_tokens[b] .. cu_tokens[b + 1]
+ * positions, slots [max_tokens] int32: of every packed row its position in the request and its slot,
+ *      page * page_size + row; rows behind the last request get -1
+ * Recorded as HS2_ERR_DEVICE_BOUNDS, with the call otherwise carried out: a length or an end outside
+ * [0, max_pages * page_size] and a request whose pages the free list cannot give (requests are served in
+ * order, while it lasts; those that need none always are): such a request keeps its length, its rows get
+ * slot -1; more new tokens than max_tokens (the rows past it are not written, nor the table entries that
+ * they would begin); more free pages than the ring holds (none is given back).
+ * Supported: 1 <= B <= 4096. Workspace: hs2_page_table_update_workspace_bytes (zero-filled before its
+ * first use).
+ */
+HS2_API size_t hs2_page_table_update_workspace_bytes(void);
+HS2_API hs2_status hs2_page_table_update(int32_t* page_table, int B, int max_pages, const int32_t* lens,
+                                         const int32_t* delta, int32_t* free_ring, int ring_size,
+                                         const int32_t* free_state, int page_size, int max_tokens, int32_t* lens_out,
+                                         int32_t* free_state_out, int32_t* cu_tokens, int32_t* positions,
+                                         int32_t* slots, void* workspace, size_t workspace_bytes, hs2_stream stream);
+
+/* ---------------------------------------------------------------------------------
+ * Decode attention over a paged cache, without selection
+ * ---------------------------------------------------------------------------------
+ * For a model's other layers (grouped heads, sliding windows, any page size): one query per sequence, no
+ * indices. The lengths stay on the device, so a captured launch serves any of them.
+ * Q [B, 1, Hq, d] bf16; query head h reads key head h / (Hq / Hk)
+ * K_pages, V_pages  pools with strides as for hs2_qk_norm_rope_paged; bf16, or with e4m3 != 0 codes (the
+ *      cache is k_scale * K8, v_scale * V8)
+ * page_table [B, max_pages] int32, lens [B] int32: DEVICE. Sequence b's keys are its tokens
+ *      max(0, lens[b] - window) .. lens[b] - 1 (window == 0: all). Only table entries of pages with such a
+ *      key are read, and other rows may hold anything. lens[b] == 0: out is 0, lse -infinity. An id
+ *      outside [0, n_pages) (its rows read as 0) and a length outside [0, max_pages * page_size] (taken
+ *      as 0) are recorded as HS2_ERR_DEVICE_BOUNDS
+ * scale  positive and finite
+ * out [B, 1, Hq, d] bf16; lse [B, 1, Hq] fp32 natural log, or NULL
+ * The split of the work depends on the lengths only, and partial results are joined in a fixed order.
+ * Supported: d = 128, or d = 64 with a bf16 cache; Hq / Hk <= 64; page_size % 16 == 0. Workspace:
+ * hs2_paged_attn_workspace_bytes.
+ */
+HS2_API size_t hs2_paged_attn_workspace_bytes(int B, int Hq, int Hk, int d);
+HS2_API hs2_status hs2_paged_attn(const hs2_bf16* Q, const void* K_pages, const void* V_pages,
+                                  const long long* k_page_strides, const long long* v_page_strides, int n_pages,
+                                  int page_size, const int32_t* page_table, int max_pages, const int32_t* lens, int B,
+                                  int Hq, int Hk, int d, int e4m3, float k_scale, float v_scale, float scale, int window,
+                                  hs2_bf16* out, float* lse, void* workspace, size_t workspace_bytes,
+                                  hs2_stream stream);
+
+/* ---------------------------------------------------------------------------------
  * Device status
  * ---------------------------------------------------------------------------------
  * hs2_read_device_status: waits for `stream`, reads the status word of `workspace` and

@@ -9,6 +9,12 @@ this package fails loudly if the library cannot be loaded.
     out2 = sparse_attn(q2, k, v, idx)                     # a sparse layer (KV Reuse)
     kv = bridge_kv_proj(h, w)                             # KV Bridging projection
 
+and around them, the operators of a serving step over a paged cache:
+
+    lens, free, cu, pos, slots = page_table_update(...)   # page tables and slots from the lengths
+    q = qk_norm_rope_paged(q, k, v, pos, slots, ...)      # head norms, rotation, rows into the pages
+    out, lse = paged_attn(q, k_pages, v_pages, table, lens)  # a layer without selection
+
 Tensors: q [B, Lq, H, d] bf16, k/v [B, Lk, d] bf16 (one K/V head), idx [B, Lq, S] int32,
 h [T, hidden] bf16, w [n_layers, 2, hidden, d] bf16 -> kv [n_layers, 2, T, d] bf16.
 """
@@ -98,6 +104,27 @@ def _load_library() -> ctypes.CDLL:
     lib.hs2_bridge_kv_proj_workspace_bytes.restype = sz
     lib.hs2_bridge_kv_proj.argtypes = [P, i32, i32, P, i32, i32, P, P, sz, P]
     lib.hs2_bridge_kv_proj.restype = i32
+    lib.hs2_qk_norm_rope.argtypes = [P, P, ll, ll, ll, ll, P, P] + [i32] * 6 + [f32, f32, P, P, i32, P, P, P]
+    lib.hs2_qk_norm_rope.restype = i32
+    lib.hs2_qk_norm_rope_bwd_workspace_bytes.argtypes = [i32] * 4
+    lib.hs2_qk_norm_rope_bwd_workspace_bytes.restype = sz
+    lib.hs2_qk_norm_rope_bwd.argtypes = [P, P, ll, ll, ll, ll, P, P] + [i32] * 6 + [f32, f32, P, P, i32, P, P, i32, P, P,
+                                                                                 P, P, P, sz, P]
+    lib.hs2_qk_norm_rope_bwd.restype = i32
+    lib.hs2_qk_norm_rope_paged_workspace_bytes.argtypes = []
+    lib.hs2_qk_norm_rope_paged_workspace_bytes.restype = sz
+    lib.hs2_qk_norm_rope_paged.argtypes = [P, P, P, ll, ll, ll, ll, ll, ll, P, P, P] + [i32] * 6 + [
+        f32, f32, P, P, i32, P, P, P, P, P, i32, i32, i32, f32, f32, P, sz, P]
+    lib.hs2_qk_norm_rope_paged.restype = i32
+    lib.hs2_page_table_update_workspace_bytes.argtypes = []
+    lib.hs2_page_table_update_workspace_bytes.restype = sz
+    lib.hs2_page_table_update.argtypes = [P, i32, i32, P, P, P, i32, P, i32, i32, P, P, P, P, P, P, sz, P]
+    lib.hs2_page_table_update.restype = i32
+    lib.hs2_paged_attn_workspace_bytes.argtypes = [i32] * 4
+    lib.hs2_paged_attn_workspace_bytes.restype = sz
+    lib.hs2_paged_attn.argtypes = [P, P, P, P, P, i32, i32, P, i32, P, i32, i32, i32, i32, i32, f32, f32, f32, i32, P, P,
+                                   P, sz, P]
+    lib.hs2_paged_attn.restype = i32
     lib.hs2_read_device_status.argtypes = [P, P]
     lib.hs2_read_device_status.restype = i32
     lib.hs2_clear_device_status.argtypes = [P, P]
@@ -135,6 +162,8 @@ def _load_marshalling():
     spec.loader.exec_module(mod)
     addr = lambda f: ctypes.cast(f, ctypes.c_void_p).value
     mod.set_entries(addr(lib.hs2_full_attn_select), addr(lib.hs2_sparse_attn))
+    mod.set_cache_entries(addr(lib.hs2_qk_norm_rope), addr(lib.hs2_qk_norm_rope_bwd), addr(lib.hs2_qk_norm_rope_paged),
+                          addr(lib.hs2_page_table_update), addr(lib.hs2_paged_attn))
     return mod
 
 
@@ -634,6 +663,202 @@ def bridge_kv_proj(h, w, *, out=None, workspace=None, stream=None):
     return out
 
 
+# -------------------------------------------------------------------------------------------------
+# around the paged cache: head norms and rotation, page tables, attention without selection. These
+# calls check their tensors in the C++ marshalling module (built with the library).
+# -------------------------------------------------------------------------------------------------
+def _marshal():
+    if _fast is None:
+        raise ImportError("the argument-marshalling module is not built: run long_context_mqa_b200/_build.py")
+    return _fast
+
+
+def _stream_on(stream, t: torch.Tensor) -> int:
+    if stream is not None and stream.device != t.device:
+        raise ValueError(f"the stream is on {stream.device}, the tensors on {t.device}")
+    return _stream_ptr(stream, t) if t.is_cuda else 0  # (a host tensor fails the checks in C++)
+
+
+def _stream_workspace(nbytes: int, t: torch.Tensor, key: str, stream, ptr: int) -> torch.Tensor:
+    """The cached workspace of (device, op, stream): calls on different streams do not share one. A
+    captured graph outlives the cache's choice of a buffer, so while capturing the caller gives one."""
+    if not t.is_cuda:
+        raise ValueError("the tensors must be CUDA tensors")
+    if stream is None:
+        capturing = torch.cuda.is_current_stream_capturing()
+    else:
+        with torch.cuda.stream(stream):
+            capturing = torch.cuda.is_current_stream_capturing()
+    if capturing:
+        raise ValueError("give a workspace of your own while capturing a graph")
+    k = (t.device, key, ptr)
+    ws = _ws_cache.get(k)
+    if ws is None or ws.numel() < nbytes:
+        with _ws_lock, torch.cuda.device(t.device), torch.cuda.stream(stream):
+            ws = torch.zeros(max(nbytes, 256), dtype=torch.uint8, device=t.device)
+            _ws_cache[k] = ws
+    return ws
+
+
+def rope_frequencies(rot: int, base: float = 10000.0, *, scaling: str | None = None, factor: float = 1.0,
+                     original_len: int = 0, beta_fast: float = 32.0, beta_slow: float = 1.0, device="cuda"):
+    """(inv_freq, mscale) for qk_norm_rope: inv_freq [rot / 2] float64 on `device`, f_i = base^(-2 i / rot).
+
+    scaling: None, or how the positions of a context `factor` times longer are fitted in:
+      "linear"  f_i / factor (positions interpolated)
+      "ntk"     the base raised to base * factor^(rot / (rot - 2)): the slowest pair is interpolated by
+                `factor`, the fastest keeps its frequency
+      "yarn"    by the turns r_i = original_len f_i / 2 pi that a pair makes over the original length: g f_i +
+                (1 - g) f_i / factor with g = (r_i - beta_slow) / (beta_fast - beta_slow) clamped to [0, 1], and
+                mscale = 0.1 ln(factor) + 1
+    """
+    if rot < 2 or rot % 2 or not base > 0 or not factor >= 1:
+        raise ValueError("rot must be even and positive, base positive, factor at least 1")
+    if scaling == "ntk":
+        if rot < 4:
+            raise ValueError("ntk scaling needs rot >= 4")
+        base = base * factor ** (rot / (rot - 2))
+    f = base ** (-torch.arange(0, rot, 2, dtype=torch.float64) / rot)
+    mscale = 1.0
+    if scaling == "linear":
+        f = f / factor
+    elif scaling == "yarn":
+        if original_len < 1 or not beta_fast > beta_slow:
+            raise ValueError("yarn scaling needs original_len and beta_fast > beta_slow")
+        g = ((original_len * f / (2 * math.pi) - beta_slow) / (beta_fast - beta_slow)).clamp(0, 1)
+        f = g * f + (1 - g) * f / factor
+        mscale = 0.1 * math.log(factor) + 1.0
+    elif scaling not in (None, "ntk"):
+        raise ValueError(f"scaling must be None, 'linear', 'ntk' or 'yarn', got {scaling!r}")
+    return f.to(device), mscale
+
+
+def qk_norm_rope(q, k, positions, inv_freq, *, q_weight=None, k_weight=None, eps=1e-6, interleaved=False, mscale=1.0,
+                 q_out=None, k_out=None, stream=None):
+    """Norm of every query and key head and the position rotation, in one pass (hs2_qk_norm_rope).
+
+    q [T,Hq,d] or [B,L,Hq,d] bf16, k with the same leading dims and [Hk,d] or (one head) [d], or None
+    (a layer that reuses another's cache); any strides whose heads start on 16-byte boundaries, such as
+    the slices of a fused projection's rows. positions: int32, the leading dims; inv_freq [rot/2]
+    float64 (rope_frequencies); q_weight, k_weight [d] bf16 or float32, both or neither (no norm).
+    Returns (q_out, k_out), bf16, contiguous, shaped like q and k.
+    """
+    m = _marshal()
+    q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device) if q_out is None else q_out
+    if k is not None and k_out is None:
+        k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
+    _check(m.qk_norm_rope(q, k, positions, inv_freq, q_weight, k_weight, eps, interleaved, mscale, q_out, k_out,
+                          _stream_on(stream, q)), "hs2_qk_norm_rope")
+    return q_out, k_out
+
+
+def qk_norm_rope_bwd_workspace_bytes(T, Hq, Hk, d) -> int:
+    return int(lib.hs2_qk_norm_rope_bwd_workspace_bytes(T, Hq, Hk, d))
+
+
+def qk_norm_rope_bwd(q, k, positions, inv_freq, dq_out, dk_out, *, q_weight=None, k_weight=None, eps=1e-6,
+                     interleaved=False, mscale=1.0, dq=None, dk=None, dq_weight=None, dk_weight=None, workspace=None,
+                     stream=None):
+    """Backward of qk_norm_rope (hs2_qk_norm_rope_bwd): the forward's arguments, then the gradients of its
+    outputs: dq_out bf16, dk_out bf16 or float32 (as full_attn_bwd gives it), contiguous.
+
+    Returns (dq, dk, dq_weight, dk_weight): bf16 shaped like q and k, float32 [d] (None without weights).
+    """
+    m = _marshal()
+    new = lambda t: torch.empty(t.shape, dtype=torch.bfloat16, device=t.device)
+    dq = new(q) if dq is None else dq
+    dk = new(k) if dk is None and k is not None else dk
+    if q_weight is not None and dq_weight is None:
+        dq_weight = torch.empty(q.shape[-1], dtype=torch.float32, device=q.device)
+    if k_weight is not None and dk_weight is None:
+        dk_weight = torch.empty(q.shape[-1], dtype=torch.float32, device=q.device)
+    st = _stream_on(stream, q)
+    if workspace is None:
+        heads = 0 if k is None else k.shape[-2] if k.dim() == q.dim() else 1
+        nbytes = qk_norm_rope_bwd_workspace_bytes(q.shape[:-2].numel(), q.shape[-2], heads, q.shape[-1])
+        workspace = _stream_workspace(nbytes, q, "rope_bwd", stream, st)
+    _check(m.qk_norm_rope_bwd(q, k, positions, inv_freq, dq_out, dk_out, q_weight, k_weight, eps, interleaved, mscale, dq,
+                              dk, dq_weight, dk_weight, workspace, st), "hs2_qk_norm_rope_bwd")
+    return dq, dk, dq_weight, dk_weight
+
+
+def _scales(k_scale, v_scale):
+    if (k_scale is None) != (v_scale is None):
+        raise ValueError("give k_scale and v_scale (an e4m3 cache) or neither")
+    return (False, 1.0, 1.0) if k_scale is None else (True, float(k_scale), float(v_scale))
+
+
+def qk_norm_rope_paged(q, k, v, positions, slots, k_pages, v_pages, inv_freq, *, q_weight=None, k_weight=None, eps=1e-6,
+                       interleaved=False, mscale=1.0, k_scale=None, v_scale=None, q_out=None, workspace=None, stream=None):
+    """qk_norm_rope for serving (hs2_qk_norm_rope_paged): the rotated keys and the values v (shaped like k) go
+    into the cache rows slots[t] = page * page_size + row of the pools k_pages, v_pages [n_pages,page,Hk,d]
+    (or [n_pages,page,d]): bf16, or uint8 e4m3 codes when k_scale and v_scale are given.
+
+    A token with a negative slot is padding: nothing of it is read or written. Returns q_out.
+    """
+    m = _marshal()
+    f8, ks, vs = _scales(k_scale, v_scale)
+    q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device) if q_out is None else q_out
+    st = _stream_on(stream, q)
+    if workspace is None:
+        workspace = _stream_workspace(256, q, "rope_paged", stream, st)
+    _check(m.qk_norm_rope_paged(q, k, v, positions, slots, k_pages, v_pages, inv_freq, q_weight, k_weight, eps,
+                                interleaved, mscale, f8, ks, vs, q_out, workspace, st), "hs2_qk_norm_rope_paged")
+    return q_out
+
+
+def page_table_update(page_table, lens, delta, free_ring, free_state, page_size, max_tokens, *, lens_out=None,
+                      free_state_out=None, cu_tokens=None, positions=None, slots=None, workspace=None, stream=None):
+    """Page tables, slots and positions of one step from the requests' lengths (hs2_page_table_update).
+
+    page_table [B,max_pages], lens [B], delta [B] (tokens gained; negative: given back), free_ring [at least the
+    pool's pages], free_state [2] (head, count): int32 on the device. page_table and free_ring are updated in
+    place; lens_out and free_state_out may be lens and free_state themselves (they are new tensors otherwise).
+    Returns (lens_out, free_state_out, cu_tokens [B+1], positions [max_tokens], slots [max_tokens]).
+    """
+    m = _marshal()
+    new = lambda n: torch.empty(n, dtype=torch.int32, device=page_table.device)
+    lens_out = new(lens.shape) if lens_out is None else lens_out
+    free_state_out = new(2) if free_state_out is None else free_state_out
+    cu_tokens = new(lens.shape[0] + 1) if cu_tokens is None else cu_tokens
+    positions = new(max_tokens) if positions is None else positions
+    slots = new(max_tokens) if slots is None else slots
+    st = _stream_on(stream, page_table)
+    if workspace is None:
+        workspace = _stream_workspace(256, page_table, "page_table", stream, st)
+    _check(m.page_table_update(page_table, lens, delta, free_ring, free_state, page_size, max_tokens, lens_out,
+                               free_state_out, cu_tokens, positions, slots, workspace, st), "hs2_page_table_update")
+    return lens_out, free_state_out, cu_tokens, positions, slots
+
+
+def paged_attn_workspace_bytes(B, Hq, Hk, d) -> int:
+    return int(lib.hs2_paged_attn_workspace_bytes(B, Hq, Hk, d))
+
+
+def paged_attn(q, k_pages, v_pages, page_table, lens, *, k_scale=None, v_scale=None, scale=None, window=0, out=None,
+               lse=None, workspace=None, stream=None):
+    """Attention of one query per sequence over a paged cache, without selection (hs2_paged_attn).
+
+    q [B,1,Hq,d] bf16; k_pages, v_pages [n_pages,page,Hk,d] (or [n_pages,page,d]) bf16, or uint8 e4m3 codes with
+    k_scale and v_scale; page_table [B,max_pages] int32 and lens [B] int32 on the device; window: the newest
+    tokens that are seen (0: all). Returns (out [B,1,Hq,d] bf16, lse [B,1,Hq] float32); an empty sequence gives
+    zeros and -infinity.
+    """
+    m = _marshal()
+    f8, ks, vs = _scales(k_scale, v_scale)
+    scale = 1.0 / math.sqrt(q.shape[-1]) if scale is None else float(scale)
+    out = torch.empty_like(q) if out is None else out
+    lse = torch.empty(q.shape[:-1], dtype=torch.float32, device=q.device) if lse is None else lse
+    st = _stream_on(stream, q)
+    if workspace is None:
+        heads = k_pages.shape[2] if k_pages.dim() == 4 else 1
+        nbytes = paged_attn_workspace_bytes(q.shape[0], q.shape[-2], heads, q.shape[-1])
+        workspace = _stream_workspace(nbytes, q, "paged_attn", stream, st)
+    _check(m.paged_attn(q, k_pages, v_pages, page_table, lens, f8, ks, vs, scale, window, out, lse, workspace, st),
+           "hs2_paged_attn")
+    return out, lse
+
+
 def read_device_status(workspace: torch.Tensor, stream=None) -> int:
     """Waits for the stream and returns the status word of `workspace` (0 = ok)."""
     return int(lib.hs2_read_device_status(workspace.data_ptr(), _stream_ptr(stream)))
@@ -643,10 +868,16 @@ def clear_device_status(workspace: torch.Tensor, stream=None) -> None:
     _check(lib.hs2_clear_device_status(workspace.data_ptr(), _stream_ptr(stream)), "hs2_clear_device_status")
 
 
-def cached_workspace(key: str, device=None):
-    """The workspace the convenience calls used for `key` ("full", "sparse", "bridge")."""
+def cached_workspace(key: str, device=None, stream=None):
+    """The workspace the convenience calls used for `key` ("full", "sparse", "bridge"), or, for the calls
+    that keep one per stream, for `key` ("rope_bwd", "rope_paged", "page_table", "paged_attn") on
+    `stream` (the current one)."""
     device = torch.device("cuda", torch.cuda.current_device()) if device is None else device
-    return _ws_cache.get((device, key))
+    ws = _ws_cache.get((device, key))
+    if ws is None:
+        stream = torch.cuda.current_stream(device) if stream is None else stream
+        ws = _ws_cache.get((device, key, stream.cuda_stream))
+    return ws
 
 
 def set_wait_limit_ns(ns: int) -> None:

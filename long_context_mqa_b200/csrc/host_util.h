@@ -24,11 +24,24 @@ bool make_tmap_3d(CUtensorMap* m, const void* base, uint64_t inner, uint64_t row
 bool make_tmap_2d(CUtensorMap* m, const void* base, uint64_t inner, uint64_t rows, uint64_t row_stride_el,
                   uint32_t box_inner, uint32_t box_rows);
 
+// 4D tensor map of a page pool [n_pages, page, Hk, d], bf16 or bytes (e4m3 codes), strides in elements:
+// dims (d, page, Hk, n_pages), box (128 bytes of d, box_rows, 1, 1), 128-byte swizzle, zeros past the pool.
+bool make_tmap_pool(CUtensorMap* m, const void* base, int d, int page, int Hk, int n_pages, long long page_stride,
+                    long long row_stride, long long head_stride, int box_rows, bool f8);
+
 long long wait_limit_ns();
 int num_sms();
 bool device_is_sm100();
 
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+// Strides (page, row, head, in elements) that a page pool may have: whole 16-byte units.
+inline bool pool_strides_ok(const long long* s, int e4m3) {
+  const int unit = e4m3 ? 16 : 8;
+  for (int i = 0; i < 3; ++i)
+    if (s[i] <= 0 || s[i] % unit != 0) return false;
+  return true;
+}
 
 // Launches `kernel` on `stream`; with pdl = true the launch may begin while the previous
 // kernel on the stream is still running (the kernel must call griddep_wait() before it reads

@@ -111,6 +111,20 @@ bool make_tmap_2d(CUtensorMap* m, const void* base, uint64_t inner, uint64_t row
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS ? (tmap_store(key, *m), true) : false;
 }
 
+bool make_tmap_pool(CUtensorMap* m, const void* base, int d, int page, int Hk, int n_pages, long long page_stride,
+                    long long row_stride, long long head_stride, int box_rows, bool f8) {
+  auto enc = get_encoder();
+  if (!enc) return false;
+  const cuuint64_t eb = f8 ? 1 : 2;
+  cuuint64_t dims[4] = {(cuuint64_t)d, (cuuint64_t)page, (cuuint64_t)Hk, (cuuint64_t)n_pages};
+  cuuint64_t strides[3] = {(cuuint64_t)row_stride * eb, (cuuint64_t)head_stride * eb, (cuuint64_t)page_stride * eb};
+  cuuint32_t box[4] = {(cuuint32_t)(128 / eb), (cuuint32_t)box_rows, 1, 1};
+  cuuint32_t es[4] = {1, 1, 1, 1};
+  return enc(m, f8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims,
+             strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 static long long g_wait_ns = -1;
 long long wait_limit_ns() {
   if (g_wait_ns < 0) {

@@ -1,0 +1,762 @@
+// Attention of one new token per sequence over a paged K/V cache (no selection): query heads in groups
+// of 1..64 per key head, pages of any multiple of 16 rows, lengths on the device, an optional window.
+//
+// Per sequence, key head and query head of its group, over the keys j in [max(0, len - window), len):
+//   out = softmax(scale q.k_j) V,   lse = log sum_j exp(scale q.k_j)
+//
+// Bound by HBM: K and V are read once (4 G flops per byte of a bf16 cache at a group of G heads), so the
+// design keeps TMA loads in flight and everything else off their path. Two CTAs per SM, each a TMA
+// warp, an MMA warp and four softmax warps around one ring of 16 KB tiles:
+//   S = Q K^T      tcgen05, M = 64 (the group's heads, zero-padded), N = the tile's keys
+//   P = exp2(S c - m_tile)   the lanes that hold a head's row (two per row), to shared memory
+//   O_tile = P V   tcgen05, a fresh accumulator per tile
+//   acc = acc 2^(m - m') + O_tile 2^(m_tile - m'),  m' = max(m, m_tile)   32-bit registers
+// P is relative to its own tile's maximum, so it keeps its precision however far that maximum lies
+// below the row's (a cache with one dominant key).
+//
+// An e4m3 cache goes to the tensor core as it is (kind::f8f6f4; nothing is widened). The 16-bit
+// operand beside it is split into two e4m3 terms, hi = e4m3(x), lo = e4m3(x - hi), whose products
+// accumulate in the same accumulator: 4 + 4 significant bits, as many as a bf16 has. Q is first
+// scaled per head by a power of two so that its largest element lies in [128, 256) (elements down to
+// 2^-9 of it are exact, smaller ones are off by 2^-17 of it at most); P is scaled by 256.
+//
+// The tiles of all (sequence, key head) pairs form one line that is cut into equal ranges, one per
+// CTA, from the lengths on the device (a captured launch serves any lengths). A pair that lies in one
+// CTA's range is finished there; the others leave (m, l, acc) records that a second kernel joins in
+// the order of the ranges, so results do not vary from run to run.
+#include "host_util.h"
+#include "tc.cuh"
+
+namespace hs2 {
+namespace pattn {
+
+constexpr int NT = 192;   // TMA warp, MMA warp, four softmax warps
+constexpr int MH = 64;    // MMA rows
+constexpr int kNoPage = -2147483647 - 1;
+constexpr int MIN_TILES = 2;  // a CTA's share at least: a record costs about as much as a tile
+
+struct Params {
+  const __nv_bfloat16* q;  // [B, Hq, D]
+  __nv_bfloat16* out;      // [B, Hq, D]
+  float* lse;              // [B, Hq] or NULL
+  const int32_t *ptab, *lens;
+  int B, Hk, G, page, box, max_pages, n_pages, window;
+  float c;       // scale log2(e), times K's scale
+  float oscale;  // V's scale
+  int W;         // CTAs of the grid at most in use
+  int* pre;      // [B + 1] first tile of each sequence on the line, and the tiles in all
+  float* po;     // [W][2][G][D] records
+  float2* pml;   // [W][2][G]
+  long long wait_ns;
+  DevStatus* st;
+};
+
+template <int D, bool F8>
+struct Lay {
+  static constexpr int TILE = F8 || D == 64 ? 128 : 64;       // keys of a tile: 16 KB of K
+  static constexpr int EB = F8 ? 1 : 2;
+  static constexpr int NKB = D * EB / 128;                    // 128-byte column blocks of a cache row
+  static constexpr int SLOT = TILE * D * EB;
+  static constexpr int Q_BYTES = MH * D * 2;                  // (e4m3: hi and lo terms)
+  static constexpr int P_BYTES = MH * TILE * 2;
+  static constexpr int NR = F8 ? 4 : 5;
+  static constexpr int OFF_P = Q_BYTES, OFF_R = OFF_P + P_BYTES;
+  static constexpr int BYTES = OFF_R + NR * SLOT + 1024;
+};
+
+__device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, long long limit, volatile int* abort_flag,
+                                         DevStatus* st, unsigned where) {
+  const uint32_t a = smem_u32(bar);
+  if (mbar_try_wait(a, parity)) return true;
+  const long long t0 = globaltimer_ns();
+  while (true) {
+    if (mbar_try_wait(a, parity)) return true;
+    if (*abort_flag) return false;
+    if (globaltimer_ns() - t0 > limit) {
+      *abort_flag = 1;
+      report_status(st, kStatusTimeout, where);
+      return false;
+    }
+  }
+}
+// the whole warp waits and gets one answer
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, long long limit, volatile int* abort_flag,
+                                          DevStatus* st, unsigned where) {
+  if (__all_sync(0xffffffffu, mbar_try_wait(smem_u32(bar), parity))) return true;
+  int ok = 1;
+  if ((threadIdx.x & 31) == 0) ok = wait_bar(bar, parity, limit, abort_flag, st, where) ? 1 : 0;
+  return __shfl_sync(0xffffffffu, ok, 0) != 0;
+}
+
+__host__ __device__ constexpr uint32_t idesc_e4m3(int M, int N, int a_mn, int b_mn) {
+  return (1u << 4) | ((uint32_t)(a_mn & 1) << 15) | ((uint32_t)(b_mn & 1) << 16) | ((uint32_t)(N >> 3) << 17) |
+         ((uint32_t)(M >> 4) << 24);  // D = f32, A and B = e4m3 (0)
+}
+__device__ __forceinline__ void umma_f8(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\ttcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::
+          "r"(d_tmem), "l"(a), "l"(b), "r"(idesc), "r"(acc)
+      : "memory");
+}
+
+// two values (the first in the low half) as f16x2 -> their hi and lo e4m3 codes (the first in the low byte)
+__device__ __forceinline__ void split_e4m3(uint32_t x, uint32_t& hi, uint32_t& lo) {
+  uint16_t h, l;
+  uint32_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(h) : "r"(x));
+  asm("{.reg .b32 w;\n\tcvt.rn.f16x2.e4m3x2 w, %1;\n\tsub.rn.f16x2 %0, %2, w;}" : "=r"(r) : "h"(h), "r"(x));
+  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(l) : "r"(r));
+  hi = h;
+  lo = l;
+}
+
+// A sequence's tiles: from the one that holds its first visible key to the one that holds its last.
+// A length that the page table cannot hold counts as none.
+template <int TILE>
+__device__ __forceinline__ int seq_tiles(const Params& p, int b, int& len, int& t0, bool* bad = nullptr) {
+  len = __ldg(p.lens + b);
+  if (len < 0 || (long long)len > (long long)p.max_pages * p.page) {
+    if (bad) *bad = true;
+    len = 0;
+  }
+  const int first = p.window > 0 && len > p.window ? len - p.window : 0;
+  t0 = first / TILE;
+  return len > 0 ? (len + TILE - 1) / TILE - t0 : 0;
+}
+
+// The segments of a range [pos, end) of the line: runs of tiles of one (sequence, key head).
+template <int TILE>
+struct Walk {
+  int b, base, len, t0, n;  // the sequence, its first tile on the line, its length, first tile, tiles per head
+  int pos, end;
+  int hk, off, cnt;         // the segment: key head, first tile within the head's run, tiles
+  __device__ __forceinline__ bool next(const Params& p) {
+    while (pos < end) {
+      if (n > 0 && pos < base + p.Hk * n) {
+        hk = (pos - base) / n;
+        off = pos - base - hk * n;
+        cnt = min(n - off, end - pos);
+        pos += cnt;
+        return true;
+      }
+      base += p.Hk * n;
+      ++b;
+      if (b >= p.B) return false;
+      n = seq_tiles<TILE>(p, b, len, t0);
+    }
+    return false;
+  }
+  __device__ __forceinline__ int first_key(const Params& p) const {
+    return p.window > 0 && len > p.window ? len - p.window : 0;
+  }
+};
+
+__device__ __forceinline__ int range_start(int w, int N, int W) { return (int)((long long)w * N / W); }
+// CTAs that share N tiles
+__device__ __forceinline__ int used_ctas(int N, int W) {
+  const int most = (N + MIN_TILES - 1) / MIN_TILES;
+  return most < W ? (most > 0 ? most : 1) : W;
+}
+
+template <int D, bool F8>
+__global__ void __launch_bounds__(NT, 2) paged_attn_kernel(const __grid_constant__ CUtensorMap tmK,
+                                                           const __grid_constant__ CUtensorMap tmV, Params p) {
+  using L = Lay<D, F8>;
+  constexpr int TILE = L::TILE, NR = L::NR, NKB = L::NKB, SLOT = L::SLOT;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+  uint8_t *sQ = smem, *sP = smem + L::OFF_P, *sR = smem + L::OFF_R;
+  __shared__ __align__(8) uint64_t r_full[NR], r_empty[NR], q_ready, s_full, s_free, p_ready, o_full, drained;
+  __shared__ uint32_t tmem_base;
+  __shared__ volatile int abort_flag;
+  __shared__ int warp_sum[NT / 32], s_start[4];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int nact = (p.G + 15) / 16;  // softmax warps with heads
+  const long long limit = p.wait_ns;
+
+  if (tid == 0) {
+    for (int i = 0; i < NR; ++i) { mbar_init(&r_full[i], 1); mbar_init(&r_empty[i], 1); }
+    mbar_init(&q_ready, nact); mbar_init(&s_full, 1); mbar_init(&s_free, nact);
+    mbar_init(&p_ready, nact); mbar_init(&o_full, 1); mbar_init(&drained, 1);
+    abort_flag = 0;
+    s_start[0] = -1;
+    fence_mbar_init();
+    tma_prefetch_desc(&tmK);
+    tma_prefetch_desc(&tmV);
+  }
+  // rows of Q and P without a head stay zero
+  for (int i = tid; i < L::OFF_R / 16; i += NT) st_shared_v4(smem_u32(smem) + i * 16, 0u, 0u, 0u, 0u);
+  fence_async_smem();
+  if (warp == 1) { tmem_alloc(&tmem_base, 256); tmem_relinquish(); }
+  griddep_wait();
+  griddep_launch_dependents();
+
+  // ---- the line of tiles: each thread sums a run of sequences
+  const int per = (p.B + NT - 1) / NT;
+  int mine = 0;
+  bool bad = false;
+  for (int i = 0; i < per; ++i) {
+    const int b = tid * per + i;
+    int len, t0;
+    if (b < p.B) mine += seq_tiles<TILE>(p, b, len, t0, &bad);
+  }
+  int x = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  if (lane == 31) warp_sum[warp] = x;
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  int before = x - mine, all = 0;
+#pragma unroll
+  for (int w = 0; w < NT / 32; ++w) {
+    const int s = warp_sum[w];
+    if (w < warp) before += s;
+    all += s;
+  }
+  const int N = all * p.Hk, W = used_ctas(N, p.W), cta = blockIdx.x;
+  const int r0 = cta < W ? range_start(cta, N, W) : N, r1 = cta < W ? range_start(cta + 1, N, W) : N;
+  if (r0 < r1 && before * p.Hk <= r0 && r0 < (before + mine) * p.Hk) {
+    int at = before * p.Hk;
+    for (int i = 0; i < per; ++i) {
+      const int b = tid * per + i;
+      int len, t0;
+      const int n = seq_tiles<TILE>(p, b, len, t0);
+      if (r0 < at + n * p.Hk) {
+        s_start[0] = b; s_start[1] = at; s_start[2] = len; s_start[3] = t0;
+        break;
+      }
+      at += n * p.Hk;
+    }
+  }
+  if (cta == 0) {  // for the join
+    int at = before * p.Hk;
+    for (int i = 0; i < per; ++i) {
+      const int b = tid * per + i;
+      int len, t0;
+      if (b < p.B) {
+        p.pre[b] = at;
+        at += seq_tiles<TILE>(p, b, len, t0) * p.Hk;
+      }
+    }
+    if (tid == 0) p.pre[p.B] = N;
+    if (bad) report_status(p.st, kStatusBounds, 701);
+  }
+  __syncthreads();
+  const uint32_t tmem = tmem_base, tS = 0, tO = 128;
+  Walk<TILE> wk;
+  wk.pos = r0; wk.end = s_start[0] >= 0 ? r1 : r0;
+  wk.b = s_start[0]; wk.base = s_start[1]; wk.len = s_start[2]; wk.t0 = s_start[3];
+  wk.n = wk.len > 0 ? (wk.len + TILE - 1) / TILE - wk.t0 : 0;
+
+  if (warp == 0) {
+    // ------------------------------------------------------------------ TMA producer: lane x loads
+    // rows x * box .. of a tile (one page's), K and V of a tile from the same page ids
+    const uint64_t once = policy_evict_first();
+    const int n_box = TILE / p.box;
+    uint32_t ri = 0;
+    bool ok = true;
+    auto load = [&](const CUtensorMap* m, int pg, int row, int hk) -> bool {
+      const int s = ri % NR;
+      if (!warp_wait(&r_empty[s], ((ri / NR) & 1) ^ 1, limit, &abort_flag, p.st, 702)) return false;
+      if (lane == 0) mbar_expect_tx(&r_full[s], SLOT);
+      __syncwarp();
+      if (lane < n_box) {
+        uint8_t* dst = sR + s * SLOT + lane * p.box * 128;
+#pragma unroll
+        for (int kb = 0; kb < NKB; ++kb) {
+          asm volatile(
+              "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1, "
+              "{%3, %4, %5, %6}], [%2], %7;" ::"r"(smem_u32(dst + kb * (TILE * 128))),
+              "l"(m), "r"(smem_u32(&r_full[s])), "r"(kb * 64), "r"(row), "r"(hk), "r"(pg), "l"(once)
+              : "memory");
+        }
+      }
+      ++ri;
+      return true;
+    };
+    while (ok && wk.next(p)) {
+      const int first = wk.first_key(p);
+      const int32_t* row_ids = p.ptab + (size_t)wk.b * p.max_pages;
+      // the page of this lane's rows of tile t: one past the pool (which reads zeros) where no key of
+      // them is visible or the id is not one of the pool's
+      auto page_of = [&](int t) -> int {
+        const int k0 = t * TILE + lane * p.box;
+        if (lane >= n_box || k0 >= wk.len || k0 + p.box <= first) return kNoPage;
+        return __ldg(row_ids + k0 / p.page);
+      };
+      auto checked = [&](int pg) -> int {
+        if (pg >= 0 && pg < p.n_pages) return pg;
+        if (pg != kNoPage) report_status(p.st, kStatusBounds, 703);
+        return p.n_pages;
+      };
+      const int t_lo = wk.t0 + wk.off, t_hi = t_lo + wk.cnt;
+      int pg_next = page_of(t_lo), pg_v = 0, row_v = 0;
+      for (int t = t_lo; t < t_hi && ok; ++t) {
+        const int raw = pg_next, row = (t * TILE + lane * p.box) % p.page;
+        if (t + 1 < t_hi) pg_next = page_of(t + 1);
+        int pg = checked(raw);
+        ok = load(&tmK, pg, row, wk.hk);
+        if (ok && t > t_lo) ok = load(&tmV, pg_v, row_v, wk.hk);
+        pg_v = pg;
+        row_v = row;
+      }
+      if (ok) ok = load(&tmV, pg_v, row_v, wk.hk);
+    }
+    if (!ok)  // let the copies already issued land before the CTA exits
+      for (uint32_t i = ri > NR ? ri - NR : 0; i < ri; ++i) mbar_wait(&r_full[i % NR], (i / NR) & 1, limit);
+  } else if (warp == 1) {
+    // ------------------------------------------------------------------ MMA issuer (one thread)
+    if (lane == 0) {
+      uint32_t ri = 0, js = 0, jp = 0, nq = 0;
+      bool ok = true;
+      const uint64_t qa = sdesc(smem_u32(sQ), 16, 1024), pa = sdesc(smem_u32(sP), 16, 1024);
+      auto issue_s = [&]() -> bool {
+        const int s = ri % NR;
+        if (!wait_bar(&r_full[s], (ri / NR) & 1, limit, &abort_flag, p.st, 711)) return false;
+        if (!wait_bar(&s_free, (js & 1) ^ 1, limit, &abort_flag, p.st, 712)) return false;
+        tc_fence_after();
+        const uint64_t ka = sdesc(smem_u32(sR + s * SLOT), 16, 1024);
+        if constexpr (F8) {
+          constexpr uint32_t ID = idesc_e4m3(MH, TILE, 0, 0);
+#pragma unroll
+          for (int h = 0; h < 2; ++h)  // Q's hi and lo terms
+#pragma unroll
+            for (int kk = 0; kk < D / 32; ++kk)
+              umma_f8(tmem + tS, sdesc_at(qa, h * (MH * 128) + kk * 32), sdesc_at(ka, kk * 32), ID, h + kk > 0);
+        } else {
+          constexpr uint32_t ID = idesc_bf16(MH, TILE, 0, 0);
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk)
+            umma_ss(tmem + tS, sdesc_at(qa, (kk / 4) * (MH * 128) + (kk % 4) * 32),
+                    sdesc_at(ka, (kk / 4) * (TILE * 128) + (kk % 4) * 32), ID, kk > 0);
+        }
+        umma_commit(&s_full);
+        umma_commit(&r_empty[s]);
+        ++ri;
+        ++js;
+        return true;
+      };
+      auto issue_pv = [&]() -> bool {
+        const int s = ri % NR;
+        if (!wait_bar(&r_full[s], (ri / NR) & 1, limit, &abort_flag, p.st, 713)) return false;
+        // P is in shared memory (and the accumulator of the tile before it has been read)
+        if (!wait_bar(&p_ready, jp & 1, limit, &abort_flag, p.st, 714)) return false;
+        tc_fence_after();
+        if constexpr (F8) {
+          constexpr uint32_t ID = idesc_e4m3(MH, D, 0, 1);
+          const uint64_t va = sdesc(smem_u32(sR + s * SLOT), TILE * 128, 1024);
+#pragma unroll
+          for (int h = 0; h < 2; ++h)  // P's hi and lo terms
+#pragma unroll
+            for (int kk = 0; kk < TILE / 32; ++kk)
+              umma_f8(tmem + tO, sdesc_at(pa, h * (MH * 128) + kk * 32), sdesc_at(va, kk * 4096), ID, h + kk > 0);
+        } else {
+          constexpr uint32_t ID = idesc_bf16(MH, D, 0, 1);
+          const uint64_t va = sdesc(smem_u32(sR + s * SLOT), TILE * 128, 1024);
+#pragma unroll
+          for (int kk = 0; kk < TILE / 16; ++kk)
+            umma_ss(tmem + tO, sdesc_at(pa, (kk / 4) * (MH * 128) + (kk % 4) * 32), sdesc_at(va, kk * 2048), ID, kk > 0);
+        }
+        umma_commit(&o_full);
+        umma_commit(&r_empty[s]);
+        ++ri;
+        ++jp;
+        return true;
+      };
+      while (ok && wk.next(p)) {
+        ok = wait_bar(&q_ready, nq & 1, limit, &abort_flag, p.st, 710);
+        ++nq;
+        for (int i = 0; i < wk.cnt && ok; ++i) {
+          ok = issue_s();
+          if (ok && i > 0) ok = issue_pv();
+        }
+        if (ok) ok = issue_pv();
+      }
+      if (!ok) {  // no MMA may still be running when the CTA gives its tensor memory back
+        umma_commit(&drained);
+        mbar_wait(&drained, 0, limit);
+      }
+    }
+  } else if ((warp & 3) < nact) {
+    // ------------------------------------------------------------------ softmax: lanes l and l + 16 of
+    // warp quarter qd share head row 16 qd + l (TMEM keeps the rows of an M = 64 accumulator in the
+    // first 16 lanes of each quarter); the first takes a tile's lower keys and the head's lower
+    // columns, the second the upper ones
+    const int qd = warp & 3, row = qd * 16 + (lane & 15), half = lane >> 4;
+    const uint32_t tq = tmem + ((uint32_t)(qd * 32) << 16);
+    const int stid = qd * 32 + lane;
+    constexpr int NL = TILE / 64;  // 32-column loads of S per lane
+    constexpr int NO = D / 64;     // ... of O
+    uint32_t js = 0, jp = 0, ring = 0;
+    bool ok = true;
+    while (ok && wk.next(p)) {
+      // ---- this head's query row -> shared memory
+      float c = p.c;
+      {
+        const __nv_bfloat16* src = p.q + ((size_t)(wk.b * p.Hk + wk.hk) * p.G + row) * D + half * (D / 2);
+        uint4 w[D / 16];
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i)
+          w[i] = row < p.G ? __ldg(reinterpret_cast<const uint4*>(src) + i) : make_uint4(0u, 0u, 0u, 0u);
+        if constexpr (F8) {
+          float am = 0.f, nan = 0.f;
+#pragma unroll
+          for (int i = 0; i < D / 16; ++i) {
+            const uint32_t a[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const float v0 = __uint_as_float(a[k] << 16), v1 = __uint_as_float(a[k] & 0xFFFF0000u);
+              am = fmaxf(am, fmaxf(fabsf(v0), fabsf(v1)));
+              nan += (v0 - v0) + (v1 - v1);  // NaN when an element is infinite or NaN
+            }
+          }
+          am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, 16));
+          nan += __shfl_xor_sync(0xffffffffu, nan, 16);
+          // am 2^e in [128, 256)
+          int e = 134 - (int)(__float_as_uint(am) >> 23);  // 127 + 7 - biased exponent
+          e = am > 0.f ? (e < -120 ? -120 : e > 120 ? 120 : e) : 0;
+          const float up = __uint_as_float((uint32_t)(127 + e) << 23);
+          c = p.c * __uint_as_float((uint32_t)(127 - e) << 23) + nan;
+#pragma unroll
+          for (int i = 0; i < D / 16; i += 2) {
+            uint32_t hi[4], lo[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const uint4& ww = w[i + k / 2];
+              const uint32_t a = k % 2 ? ww.z : ww.x, b2 = k % 2 ? ww.w : ww.y;
+              uint32_t h0, l0, h1, l1;
+              // (a bf16 element times a power of two below 256 is an f16 value, or too small to matter)
+              split_e4m3(pack_f16x2(__uint_as_float(a << 16) * up, __uint_as_float(a & 0xFFFF0000u) * up), h0, l0);
+              split_e4m3(pack_f16x2(__uint_as_float(b2 << 16) * up, __uint_as_float(b2 & 0xFFFF0000u) * up), h1, l1);
+              hi[k] = h0 | (h1 << 16);
+              lo[k] = l0 | (l1 << 16);
+            }
+            const uint32_t dst = smem_u32(sQ) + sw128_off(row, half * (D / 32) + i / 2);
+            st_shared_v4(dst, hi[0], hi[1], hi[2], hi[3]);
+            st_shared_v4(dst + MH * 128, lo[0], lo[1], lo[2], lo[3]);
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < D / 16; ++i) {
+            const int ch = half * (D / 16) + i;
+            st_shared_v4(smem_u32(sQ) + (ch / 8) * (MH * 128) + sw128_off(row, ch % 8), w[i].x, w[i].y, w[i].z, w[i].w);
+          }
+        }
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&q_ready);
+      }
+      float m_run = -INFINITY, l_run = 0.f, al = 1.f, be = 0.f;  // al, be: factors of the last tile's O
+      float acc[NO][32];
+#pragma unroll
+      for (int i = 0; i < NO; ++i)
+#pragma unroll
+        for (int k = 0; k < 32; ++k) acc[i][k] = 0.f;
+      // acc = acc al + O be for the tile whose PV was issued last
+      auto add_o = [&]() -> bool {
+        if (!warp_wait(&o_full, jp & 1, limit, &abort_flag, p.st, 721)) return false;
+        ++jp;
+        tc_fence_after();
+#pragma unroll
+        for (int i = 0; i < NO; ++i) {
+          float o[32];
+          tmem_ld16x2_32<D / 2>(tq + tO + i * 32, o);
+          tmem_ld_wait();
+#pragma unroll
+          for (int k = 0; k < 32; ++k) acc[i][k] = acc[i][k] * al + o[k] * be;
+        }
+        tc_fence_before();
+        return true;
+      };
+      const int first = wk.first_key(p);
+      const int t_lo = wk.t0 + wk.off;
+      for (int i = 0; i < wk.cnt && ok; ++i) {
+        const int key0 = (t_lo + i) * TILE;
+        const int lo = max(first - key0, 0), hi = min(wk.len - key0, TILE);  // visible keys of the tile
+        if (!warp_wait(&s_full, js & 1, limit, &abort_flag, p.st, 720)) { ok = false; break; }
+        ++js;
+        tc_fence_after();
+        float sv[NL][32];
+#pragma unroll
+        for (int j = 0; j < NL; ++j) tmem_ld16x2_32<TILE / 2>(tq + tS + j * 32, sv[j]);
+        tmem_ld_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&s_free);
+        if (lo > 0 || hi < TILE) {
+          const int a = lo - half * (TILE / 2), b2 = hi - half * (TILE / 2);
+#pragma unroll
+          for (int j = 0; j < NL; ++j)
+#pragma unroll
+            for (int k = 0; k < 32; ++k) sv[j][k] = j * 32 + k >= a && j * 32 + k < b2 ? sv[j][k] : -INFINITY;
+        }
+        float rm = max32(sv[0]);
+#pragma unroll
+        for (int j = 1; j < NL; ++j) rm = fmaxf(rm, max32(sv[j]));
+        rm = fmaxf(rm, __shfl_xor_sync(0xffffffffu, rm, 16));
+        const float mt = rm * c;
+        const float neg = mt == -INFINITY ? 0.f : F8 ? 8.f - mt : -mt;
+        float la = 0.f, lb = 0.f;
+        uint32_t pk[NL * 16];  // bf16 pairs; e4m3: the hi codes of four keys, then the lo codes
+#pragma unroll
+        for (int j = 0; j < NL; ++j)
+#pragma unroll
+          for (int k = 0; k < 32; k += 4) {
+            float e[4];
+            ffma2(e[0], e[1], sv[j][k], sv[j][k + 1], c, c, neg, neg);
+            ffma2(e[2], e[3], sv[j][k + 2], sv[j][k + 3], c, c, neg, neg);
+#pragma unroll
+            for (int y = 0; y < 4; ++y) e[y] = fast_exp2(e[y]);
+            fadd2(la, lb, la, lb, e[0], e[1]);
+            fadd2(la, lb, la, lb, e[2], e[3]);
+            if constexpr (F8) {
+              uint32_t h0, l0, h1, l1;
+              split_e4m3(pack_f16x2(e[0], e[1]), h0, l0);
+              split_e4m3(pack_f16x2(e[2], e[3]), h1, l1);
+              pk[j * 8 + k / 4] = h0 | (h1 << 16);
+              pk[NL * 8 + j * 8 + k / 4] = l0 | (l1 << 16);
+            } else {
+              pk[j * 16 + k / 2] = pack_bf16x2(e[0], e[1]);
+              pk[j * 16 + k / 2 + 1] = pack_bf16x2(e[2], e[3]);
+            }
+          }
+        // the last tile's product before P is overwritten
+        if (i > 0 && !add_o()) { ok = false; break; }
+        // factors of this tile's product
+        const float mn = fmaxf(m_run, mt);
+        al = m_run == mn ? 1.f : m_run == -INFINITY ? 0.f : fast_exp2(m_run - mn);
+        be = mt == -INFINITY ? 0.f : (F8 ? 0.00390625f : 1.f) * fast_exp2(mt - mn);
+        l_run = l_run * al + (la + lb) * be;
+        m_run = mn;
+        // ---- P -> shared memory, K-major
+        if constexpr (F8) {
+#pragma unroll
+          for (int y = 0; y < NL * 2; ++y) {
+            const uint32_t dst = smem_u32(sP) + sw128_off(row, half * (NL * 2) + y);
+            st_shared_v4(dst, pk[4 * y], pk[4 * y + 1], pk[4 * y + 2], pk[4 * y + 3]);
+            st_shared_v4(dst + MH * 128, pk[NL * 8 + 4 * y], pk[NL * 8 + 4 * y + 1], pk[NL * 8 + 4 * y + 2],
+                         pk[NL * 8 + 4 * y + 3]);
+          }
+        } else {
+#pragma unroll
+          for (int y = 0; y < NL * 4; ++y) {
+            const int ch = half * (NL * 4) + y;
+            st_shared_v4(smem_u32(sP) + (ch / 8) * (MH * 128) + sw128_off(row, ch % 8), pk[4 * y], pk[4 * y + 1],
+                         pk[4 * y + 2], pk[4 * y + 3]);
+          }
+        }
+        if (lo > 0 || hi < TILE) {
+          // rows of V that no key is in may hold anything, and 0 times an infinity or a NaN is not 0
+          const uint32_t vi = ring + (i == wk.cnt - 1 ? 2 * wk.cnt - 1 : 2 * i + 2);
+          if (!warp_wait(&r_full[vi % NR], (vi / NR) & 1, limit, &abort_flag, p.st, 722)) { ok = false; break; }
+          const uint32_t v = smem_u32(sR + (vi % NR) * SLOT);
+          for (int ch = stid; ch < SLOT / 16; ch += nact * 32) {
+            const int r = (ch / 8) % TILE;
+            if (r < lo || r >= hi) st_shared_v4(v + ch * 16, 0u, 0u, 0u, 0u);
+          }
+        }
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_ready);
+      }
+      ring += 2 * wk.cnt;
+      if (!ok || !add_o()) { ok = false; break; }
+      l_run += __shfl_xor_sync(0xffffffffu, l_run, 16);
+      const size_t head = (size_t)(wk.b * p.Hk + wk.hk) * p.G + row;
+      if (row < p.G && wk.cnt == wk.n) {  // the whole row
+        const float inv = l_run == 0.f ? 0.f : p.oscale / l_run;
+        uint4* dst = reinterpret_cast<uint4*>(p.out + head * D + half * (D / 2));
+#pragma unroll
+        for (int i = 0; i < NO; ++i)
+#pragma unroll
+          for (int k = 0; k < 32; k += 8)
+            dst[i * 4 + k / 8] = make_uint4(pack_bf16x2(acc[i][k] * inv, acc[i][k + 1] * inv),
+                                            pack_bf16x2(acc[i][k + 2] * inv, acc[i][k + 3] * inv),
+                                            pack_bf16x2(acc[i][k + 4] * inv, acc[i][k + 5] * inv),
+                                            pack_bf16x2(acc[i][k + 6] * inv, acc[i][k + 7] * inv));
+        if (p.lse && half == 0) p.lse[head] = (m_run + log2f(l_run)) * 0.69314718055994531f;
+      } else if (row < p.G) {  // a record: slot 0 where the segment starts the CTA's range, else slot 1 (it ends it)
+        const int at = wk.base + wk.hk * wk.n + wk.off;
+        const size_t rec = ((size_t)cta * 2 + (at == r0 ? 0 : 1)) * p.G + row;
+        float4* dst = reinterpret_cast<float4*>(p.po + rec * D + half * (D / 2));
+#pragma unroll
+        for (int i = 0; i < NO; ++i)
+#pragma unroll
+          for (int k = 0; k < 32; k += 4)
+            dst[i * 8 + k / 4] = make_float4(acc[i][k], acc[i][k + 1], acc[i][k + 2], acc[i][k + 3]);
+        if (half == 0) p.pml[rec] = make_float2(m_run, l_run);
+      }
+      __syncwarp();
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) { tc_fence_after(); tmem_dealloc(tmem, 256); }
+}
+
+// Joins the records of the (sequence, key head) pairs that several CTAs worked on, in the order of
+// their ranges, and writes the rows of sequences without a key. One warp per head row.
+constexpr int JT = 256;
+template <int D>
+__global__ void __launch_bounds__(JT) paged_join_kernel(Params p) {
+  const int lane = threadIdx.x & 31, row = blockIdx.y * (JT / 32) + (threadIdx.x >> 5);
+  const int b = blockIdx.x / p.Hk, hk = blockIdx.x % p.Hk;
+  griddep_wait();
+  griddep_launch_dependents();
+  if (row >= p.G) return;
+  const size_t head = (size_t)blockIdx.x * p.G + row;
+  const int base = __ldcg(p.pre + b), n = (__ldcg(p.pre + b + 1) - base) / p.Hk, N = __ldcg(p.pre + p.B);
+  constexpr int VL = D / 32;  // columns of a lane
+  __nv_bfloat16* dst = p.out + head * D + lane * VL;
+  if (n == 0) {
+#pragma unroll
+    for (int i = 0; i < VL; i += 2) *reinterpret_cast<uint32_t*>(dst + i) = 0u;
+    if (lane == 0 && p.lse) p.lse[head] = -INFINITY;
+    return;
+  }
+  const int W = used_ctas(N, p.W), s = base + hk * n, e = s + n;
+  int w0 = (int)((long long)s * W / N);  // the CTA whose range holds tile s
+  while (w0 > 0 && range_start(w0, N, W) > s) --w0;
+  while (range_start(w0 + 1, N, W) <= s) ++w0;
+  if (range_start(w0 + 1, N, W) >= e) return;  // finished by that CTA
+  int w1 = w0 + 1;  // past the last one
+  while (range_start(w1, N, W) < e) ++w1;
+  const int cnt = w1 - w0;
+  // only the first can start before tile s (then its record is the second one of that CTA)
+  const int first_slot = range_start(w0, N, W) == s ? 0 : 1;
+  auto rec = [&](int i) { return ((size_t)(w0 + i) * 2 + (i == 0 ? first_slot : 0)) * p.G + row; };
+  float M = -INFINITY;
+  for (int i = lane; i < cnt; i += 32) M = fmaxf(M, __ldcg(&p.pml[rec(i)]).x);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+  float acc[VL], l = 0.f;
+#pragma unroll
+  for (int i = 0; i < VL; ++i) acc[i] = 0.f;
+  for (int i0 = 0; i0 < cnt; i0 += 32) {
+    float w = 0.f;
+    if (i0 + lane < cnt) {
+      const float2 ml = __ldcg(&p.pml[rec(i0 + lane)]);
+      w = ml.x == -INFINITY ? 0.f : fast_exp2(ml.x - M);
+      l += ml.y * w;
+    }
+    const int m = min(32, cnt - i0);
+#pragma unroll 8
+    for (int i = 0; i < m; ++i) {
+      const float wi = __shfl_sync(0xffffffffu, w, i);
+      const float* src = p.po + rec(i0 + i) * D + lane * VL;
+      if constexpr (VL == 4) {
+        const float4 o = __ldcg(reinterpret_cast<const float4*>(src));
+        acc[0] += o.x * wi; acc[1] += o.y * wi; acc[2] += o.z * wi; acc[3] += o.w * wi;
+      } else {
+        const float2 o = __ldcg(reinterpret_cast<const float2*>(src));
+        acc[0] += o.x * wi; acc[1] += o.y * wi;
+      }
+    }
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+  const float inv = l == 0.f ? 0.f : p.oscale / l;
+#pragma unroll
+  for (int i = 0; i < VL; i += 2) *reinterpret_cast<uint32_t*>(dst + i) = pack_bf16x2(acc[i] * inv, acc[i + 1] * inv);
+  if (lane == 0 && p.lse) p.lse[head] = (M + log2f(l)) * 0.69314718055994531f;
+}
+
+// -------------------------------------------------------------------------------------- host
+constexpr size_t kStatusBytes = 256;
+static size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
+
+static size_t carve(Params* p, void* ws, int B, int G, int D, int W) {
+  uint8_t* base = (uint8_t*)ws;
+  size_t off = kStatusBytes;
+  if (p) { p->st = (DevStatus*)base; p->pre = (int*)(base + off); }
+  off = up256(off + (size_t)(B + 1) * 4);
+  if (p) p->pml = (float2*)(base + off);
+  off = up256(off + (size_t)W * 2 * G * sizeof(float2));
+  if (p) p->po = (float*)(base + off);
+  return up256(off + (size_t)W * 2 * G * D * sizeof(float));
+}
+
+static int gcd(int a, int b) { return b == 0 ? a : gcd(b, a % b); }
+
+template <int D, bool F8>
+static cudaError_t launch(const CUtensorMap& tk, const CUtensorMap& tv, const Params& p, cudaStream_t st) {
+  using L = Lay<D, F8>;
+  cudaError_t e = cudaFuncSetAttribute(paged_attn_kernel<D, F8>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::BYTES);
+  if (e != cudaSuccess) return e;
+  {
+    LaunchScope ls("paged_attn", st);
+    e = launch_k(paged_attn_kernel<D, F8>, dim3(p.W), dim3(NT), L::BYTES, st, true, tk, tv, p);
+  }
+  if (e != cudaSuccess) return e;
+  LaunchScope ls("paged_join", st);
+  return launch_k(paged_join_kernel<D>, dim3(p.B * p.Hk, (p.G + JT / 32 - 1) / (JT / 32)), dim3(JT), 0, st, true, p);
+}
+
+}  // namespace pattn
+}  // namespace hs2
+
+using namespace hs2;
+
+extern "C" {
+
+static bool pattn_sizes_ok(int B, int Hq, int Hk) {
+  return B >= 0 && Hk >= 1 && Hq >= Hk && Hq % Hk == 0 && (long long)B * Hq <= 0x3FFFFFFFll;
+}
+
+size_t hs2_paged_attn_workspace_bytes(int B, int Hq, int Hk, int d) {
+  if (!pattn_sizes_ok(B, Hq, Hk) || Hq / Hk > pattn::MH || (d != 64 && d != 128)) return 0;
+  const int sms = num_sms() > 0 ? num_sms() : 148;
+  return pattn::carve(nullptr, nullptr, B, Hq / Hk, d, 2 * sms);
+}
+
+hs2_status hs2_paged_attn(const hs2_bf16* Q, const void* K_pages, const void* V_pages, const long long* k_page_strides,
+                          const long long* v_page_strides, int n_pages, int page_size, const int32_t* page_table,
+                          int max_pages, const int32_t* lens, int B, int Hq, int Hk, int d, int e4m3, float k_scale,
+                          float v_scale, float scale, int window, hs2_bf16* out, float* lse, void* workspace,
+                          size_t workspace_bytes, hs2_stream stream) {
+  if (!pattn_sizes_ok(B, Hq, Hk) || !Q || !K_pages || !V_pages || !k_page_strides || !v_page_strides || !page_table ||
+      !lens || !out || n_pages < 1 || page_size < 1 || max_pages < 1 || window < 0 ||
+      (long long)max_pages * page_size > 0x3FFFFFFFll || !(scale > 0.f && scale < INFINITY) || !aligned16(Q) ||
+      !aligned16(K_pages) || !aligned16(V_pages) || !aligned16(out))
+    return HS2_ERR_INVALID_ARG;
+  if (!pool_strides_ok(k_page_strides, e4m3) || !pool_strides_ok(v_page_strides, e4m3)) return HS2_ERR_INVALID_ARG;
+  if (e4m3 && !(k_scale > 0.f && k_scale < INFINITY && v_scale > 0.f && v_scale < INFINITY)) return HS2_ERR_INVALID_ARG;
+  const int G = Hq / Hk;
+  if (G > pattn::MH || page_size % 16 != 0 || (d != 128 && (d != 64 || e4m3)) || !device_is_sm100())
+    return HS2_ERR_UNSUPPORTED_SHAPE;
+  if (!workspace || !aligned16(workspace) || workspace_bytes < hs2_paged_attn_workspace_bytes(B, Hq, Hk, d))
+    return HS2_ERR_WORKSPACE;
+  if (B == 0) return HS2_OK;
+  const int tile = e4m3 || d == 64 ? 128 : 64;
+  pattn::Params p{};
+  p.q = (const __nv_bfloat16*)Q; p.out = (__nv_bfloat16*)out; p.lse = lse;
+  p.ptab = page_table; p.lens = lens;
+  p.B = B; p.Hk = Hk; p.G = G; p.page = page_size; p.box = pattn::gcd(page_size, tile);
+  p.max_pages = max_pages; p.n_pages = n_pages; p.window = window;
+  p.c = scale * 1.4426950408889634f * (e4m3 ? k_scale : 1.f);
+  p.oscale = e4m3 ? v_scale : 1.f;
+  p.wait_ns = wait_limit_ns();
+  // tiles that the batch can have at most: one line of 32-bit tile numbers
+  const long long span = (long long)max_pages * page_size;
+  const long long most = (long long)B * Hk * ((window > 0 && window < span ? window + tile : span) / tile + 1);
+  if (most > 0x3FFFFFFFll) return HS2_ERR_UNSUPPORTED_SHAPE;
+  p.W = 2 * num_sms();
+  pattn::carve(&p, workspace, B, G, d, p.W);
+  if (most < p.W) p.W = (int)most;
+  CUtensorMap tk, tv;
+  if (!make_tmap_pool(&tk, K_pages, d, page_size, Hk, n_pages, k_page_strides[0], k_page_strides[1], k_page_strides[2],
+                      p.box, e4m3 != 0) ||
+      !make_tmap_pool(&tv, V_pages, d, page_size, Hk, n_pages, v_page_strides[0], v_page_strides[1], v_page_strides[2],
+                      p.box, e4m3 != 0))
+    return HS2_ERR_CUDA;
+  const cudaStream_t st = (cudaStream_t)stream;
+  const cudaError_t e = e4m3 ? pattn::launch<128, true>(tk, tv, p, st)
+                             : d == 128 ? pattn::launch<128, false>(tk, tv, p, st) : pattn::launch<64, false>(tk, tv, p, st);
+  return e == cudaSuccess ? HS2_OK : HS2_ERR_CUDA;
+}
+
+}  // extern "C"
