@@ -8,15 +8,19 @@
 // Backward, g the upstream gradient rotated back (by -angle, times m), u = g w, r = rsqrt(..):
 //   dx = r (u - x r^2 mean(u x)),   dw = sum over rows of g x r.
 //
-// All of it is bound by HBM (a few flops per byte; the kernels read each row once and write it
-// once), so the layout serves the memory system: a lane owns 8 consecutive elements (one 16-byte
-// access), d/8 lanes a row, and a warp works on the rows of ONE token, so the token's cosines and
-// sines stay in registers over its heads. They are computed once per (warp, token): each lane takes
-// a share of the angles, in 64 bits as turns t * f / 2 pi reduced to [-1/2, 1/2] (a 32-bit angle of
-// position 10^6 is off by 0.06), and the lanes read theirs back from shared memory. A row's mean is
-// a shuffle reduction over its lanes, and in the half layout the partner of an element sits rot/16
-// lanes away. Loads of several rows are issued before the first is used. All arithmetic is in 32
-// bits, rounded once at the store.
+// All of it is bound by HBM (a few flops per byte; each row is read once and written once), and next to
+// that by the issue slots, so the layout spares instructions. A lane owns two groups of 4 elements
+// (8-byte accesses; d/8 lanes a row) chosen so that it holds both elements of its pairs: in the half
+// layout groups 4 i and rot/2 + 4 i, interleaved 8 i and 8 i + 4; no element moves between lanes, only
+// the row's sums do. The head weight is folded into the lane's cosines and sines,
+//   y = r (x C + partner S),   C = m w cos, S = -+ m w_partner sin,
+// 16 registers that stay over a token's heads (a warp works on the rows of ONE token), and products run
+// two to an instruction (f32x2). The angles are computed once per (warp, token), shared out over the
+// lanes, in 64 bits as turns t * f / 2 pi reduced to [-1/2, 1/2] (a 32-bit angle of position 10^6 is off
+// by 0.06). Loads of several rows are issued before the first is used. All arithmetic is in 32 bits,
+// rounded once at the store.
+#include <type_traits>
+
 #include "host_util.h"
 #include "tc.cuh"
 
@@ -34,7 +38,6 @@ struct Params {
   const void *qw, *kw;  // NULL: no norm
   int w_f32;
   int T, Hq, Hk, rot;
-  int rows;    // rows of a token: Hq + Hk, + Hk values in the paged form
   int parts;   // warps that share a token's rows
   float eps, mscale;
   __nv_bfloat16 *q_out, *k_out;  // contiguous [T, Hq, D], [T, Hk, D]
@@ -52,97 +55,106 @@ struct Params {
   float* part;  // [grid][2][D] weight gradients of each block
 };
 
-__device__ __forceinline__ void unpack8(const uint4& w, float (&x)[8]) {
-  const uint32_t a[4] = {w.x, w.y, w.z, w.w};
+// 8 values of a lane: x[0..3] its first group, x[4..7] its second
+struct V8 {
+  float x[8];
+};
+__device__ __forceinline__ void unpack4(const uint2& w, float* x) {
+  x[0] = __uint_as_float(w.x << 16);
+  x[1] = __uint_as_float(w.x & 0xFFFF0000u);
+  x[2] = __uint_as_float(w.y << 16);
+  x[3] = __uint_as_float(w.y & 0xFFFF0000u);
+}
+__device__ __forceinline__ uint2 pack4(const float* x) { return make_uint2(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3])); }
+// four floats -> e4m3 codes (the first in the low byte), rounded to nearest even, saturating at 448
+__device__ __forceinline__ uint32_t pack4_e4m3(const float* x) {
+  uint16_t lo, hi;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(x[1]), "f"(x[0]));
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(x[3]), "f"(x[2]));
+  return (uint32_t)lo | ((uint32_t)hi << 16);
+}
+__device__ __forceinline__ void fmul2(float& dx, float& dy, float ax, float ay, float bx, float by) {
+  asm("{.reg .b64 ra, rb, rd;\n\tmov.b64 ra, {%2,%3};\n\tmov.b64 rb, {%4,%5};\n\tmul.rn.f32x2 rd, ra, rb;\n\t"
+      "mov.b64 {%0,%1}, rd;}"
+      : "=f"(dx), "=f"(dy)
+      : "f"(ax), "f"(ay), "f"(bx), "f"(by));
+}
+// d = a * b + c and d = a * b, elementwise
+__device__ __forceinline__ void fma8(V8& d, const V8& a, const V8& b, const V8& c) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    x[2 * i] = __uint_as_float(a[i] << 16);
-    x[2 * i + 1] = __uint_as_float(a[i] & 0xFFFF0000u);
-  }
+  for (int i = 0; i < 8; i += 2) ffma2(d.x[i], d.x[i + 1], a.x[i], a.x[i + 1], b.x[i], b.x[i + 1], c.x[i], c.x[i + 1]);
 }
-__device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
-  return make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
-}
-// two floats -> e4m3 codes (the first in the low byte), rounded to nearest even, saturating at 448
-__device__ __forceinline__ uint32_t pack_e4m3x2(float lo, float hi) {
-  uint16_t r;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-__device__ __forceinline__ uint2 pack8_e4m3(const float (&x)[8]) {
-  return make_uint2(pack_e4m3x2(x[0], x[1]) | (pack_e4m3x2(x[2], x[3]) << 16),
-                    pack_e4m3x2(x[4], x[5]) | (pack_e4m3x2(x[6], x[7]) << 16));
-}
-__device__ __forceinline__ void load_w8(const void* w, int f32, int at, float (&x)[8]) {
-  if (!w) {
+__device__ __forceinline__ void mul8(V8& d, const V8& a, const V8& b) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = 1.f;
-  } else if (f32) {
-    const float4 a = __ldg((const float4*)((const float*)w + at)), b = __ldg((const float4*)((const float*)w + at) + 1);
-    x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w; x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
-  } else {
-    unpack8(__ldg((const uint4*)((const __nv_bfloat16*)w + at)), x);
-  }
+  for (int i = 0; i < 8; i += 2) fmul2(d.x[i], d.x[i + 1], a.x[i], a.x[i + 1], b.x[i], b.x[i + 1]);
+}
+__device__ __forceinline__ void scale8(V8& d, const V8& a, float b) {
+#pragma unroll
+  for (int i = 0; i < 8; i += 2) fmul2(d.x[i], d.x[i + 1], a.x[i], a.x[i + 1], b, b);
+}
+__device__ __forceinline__ float dot8(const V8& a, const V8& b) {
+  float s = 0.f, t = 0.f;
+#pragma unroll
+  for (int i = 0; i < 8; i += 2) ffma2(s, t, a.x[i], a.x[i + 1], b.x[i], b.x[i + 1], s, t);
+  return s + t;
 }
 
-// The rotation of one token as a lane applies it: element e of the lane's 8 belongs to pair
-// pair_of(e); cs[] holds that pair's cosine and sine times m (half layout: 8 pairs, interleaved: 4).
+// Which elements a lane owns, and its pairs: half layout, group one's element i with group two's;
+// interleaved, elements 2 i and 2 i + 1 of each group. Lanes past the rotated part own two adjacent
+// groups that pass.
 template <int D, bool INTER>
-struct Rot {
-  static constexpr int LPR = D / 8;            // lanes of a row
-  static constexpr int NP = INTER ? 4 : 8;     // pairs a lane meets
-  float c[NP], s[NP];
-  int partner;   // the lane that holds the other half of this lane's pairs (half layout)
-  bool on;       // this lane's elements are rotated
-
-  __device__ __forceinline__ void init(int lane, int rot) {
-    const int li = lane % LPR, hl = rot / 16;
-    on = li * 8 < rot;
-    partner = !on ? lane : li < hl ? lane + hl : lane - hl;
-  }
-  // the whole warp: token position t; `sc` is this warp's [MAX_HALF] buffer
-  __device__ __forceinline__ void angles(int t, const double* inv_freq, int rot, float mscale, int lane, float2* sc) {
-    const int half = rot / 2;
-    __syncwarp();
-    for (int i = lane; i < half; i += 32) {
-      const double turns = (double)t * __ldg(inv_freq + i) * 0.15915494309189533577;  // 1 / (2 pi)
-      float sn, cn;
-      sincospif((float)(2.0 * (turns - rint(turns))), &sn, &cn);
-      sc[i] = make_float2(cn * mscale, sn * mscale);
-    }
-    __syncwarp();
+struct Lane {
+  static constexpr int LPR = D / 8;  // lanes of a row
+  int a, b;                          // first element of each group
+  bool on;                           // its elements are rotated
+  __device__ __forceinline__ Lane(int lane, int rot) {
     const int li = lane % LPR;
-    if (on) {
-      const int first = INTER ? li * 4 : (li * 8 < half ? li * 8 : li * 8 - half);
-      const float sg = !INTER && li * 8 < half ? -1.f : 1.f;  // first half: a cos - b sin
+    on = li * 8 < rot;
+    a = INTER || !on ? li * 8 : li * 4;
+    b = INTER || !on ? a + 4 : rot / 2 + li * 4;
+  }
+  __device__ __forceinline__ static V8 swap(const V8& x) {  // each element's partner
+    V8 y;
 #pragma unroll
-      for (int e = 0; e < NP; ++e) {
-        const float2 x = sc[first + e];
-        c[e] = x.x;
-        s[e] = x.y * sg;
-      }
+    for (int i = 0; i < 8; ++i) y.x[i] = x.x[INTER ? i ^ 1 : i ^ 4];
+    return y;
+  }
+  // cosines, and sines signed as the rotation applies them (y = x c + partner s), both times m
+  __device__ __forceinline__ void read(const float2* sc, V8& c, V8& s) const {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float2 v = on ? sc[INTER ? a / 2 + i / 2 : a + i % 4] : make_float2(1.f, 0.f);
+      const bool first = INTER ? i % 2 == 0 : i < 4;
+      c.x[i] = v.x;
+      s.x[i] = first ? -v.y : v.y;
     }
   }
-  // x -> its rotation (dir = 1) or the transpose (dir = -1); every lane of the warp takes part
-  __device__ __forceinline__ void apply(float (&x)[8], float dir) const {
-    if (INTER) {
-      if (on) {
+  __device__ __forceinline__ void weights(const void* w, int f32, V8& v) const {
+    if (!w) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float a = x[2 * i], b = x[2 * i + 1], sn = s[i % NP] * dir;
-          x[2 * i] = a * c[i % NP] - b * sn;
-          x[2 * i + 1] = b * c[i % NP] + a * sn;
-        }
-      }
+      for (int i = 0; i < 8; ++i) v.x[i] = 1.f;
+    } else if (f32) {
+      const float4 p = __ldg((const float4*)((const float*)w + a)), q = __ldg((const float4*)((const float*)w + b));
+      v.x[0] = p.x; v.x[1] = p.y; v.x[2] = p.z; v.x[3] = p.w;
+      v.x[4] = q.x; v.x[5] = q.y; v.x[6] = q.z; v.x[7] = q.w;
     } else {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float o = __shfl_sync(0xffffffffu, x[e], partner);
-        if (on) x[e] = x[e] * c[e % NP] + o * (s[e % NP] * dir);
-      }
+      unpack4(__ldg((const uint2*)((const __nv_bfloat16*)w + a)), v.x);
+      unpack4(__ldg((const uint2*)((const __nv_bfloat16*)w + b)), v.x + 4);
     }
   }
 };
+
+// The whole warp: cosines and sines of position t, times m, into the warp's buffer
+__device__ __forceinline__ void angles(int t, const double* inv_freq, int half, float mscale, int lane, float2* sc) {
+  __syncwarp();
+  for (int i = lane; i < half; i += 32) {
+    const double turns = (double)t * __ldg(inv_freq + i) * 0.15915494309189533577;  // 1 / (2 pi)
+    float sn, cn;
+    sincospif((float)(2.0 * (turns - rint(turns))), &sn, &cn);
+    sc[i] = make_float2(cn * mscale, sn * mscale);
+  }
+  __syncwarp();
+}
 
 template <int LPR>
 __device__ __forceinline__ float row_sum(float v) {
@@ -151,13 +163,13 @@ __device__ __forceinline__ float row_sum(float v) {
   return v;
 }
 
-// One warp per (token, part): the part's rows in passes of 32 / LPR rows, U passes in flight.
+// One warp per (token, part): a part is a run of the token's passes, a pass 32 / LPR rows: first the
+// passes of the queries, then the keys', then (paged) the values'.
 template <int D, bool INTER, bool PAGED, bool F8>
-__global__ void __launch_bounds__(NT) rope_fwd_kernel(Params p) {
+__global__ void __launch_bounds__(NT, 4) rope_fwd_kernel(Params p) {
   constexpr int LPR = D / 8, RPW = 32 / LPR, U = 4;
   __shared__ float2 sc[NW][MAX_HALF];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int li = lane % LPR, sub = lane / LPR;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = lane / LPR;
   const long long item = (long long)blockIdx.x * NW + warp;
   griddep_wait();
   griddep_launch_dependents();
@@ -168,9 +180,7 @@ __global__ void __launch_bounds__(NT) rope_fwd_kernel(Params p) {
     slot = __ldg(p.slots + t);
     if (slot < 0) return;  // a padding row: nothing of it is read or written
   }
-  Rot<D, INTER> rot;
-  rot.init(lane, p.rot);
-  rot.angles(__ldg(p.pos + t), p.inv_freq, p.rot, p.mscale, lane, sc[warp]);
+  const Lane<D, INTER> own(lane, p.rot);
   long long kc = -1, vc = -1;  // the cache rows of this token
   if (PAGED) {
     const int pg = slot / p.page, r = slot - pg * p.page;
@@ -181,62 +191,87 @@ __global__ void __launch_bounds__(NT) rope_fwd_kernel(Params p) {
       report_status(p.st, kStatusBounds, 501);
     }
   }
-  const int n_pass = (p.rows + RPW - 1) / RPW;
+  const int nq = (p.Hq + RPW - 1) / RPW, nk = (p.Hk + RPW - 1) / RPW;  // passes
+  const int n_pass = nq + (PAGED ? 2 : 1) * nk;
   const int per = (n_pass + p.parts - 1) / p.parts;
-  const int p1 = min(n_pass, (part + 1) * per);
-  float wq[8], wk[8];
-  load_w8(p.qw, p.w_f32, li * 8, wq);
-  load_w8(p.kw, p.w_f32, li * 8, wk);
-  for (int p0 = part * per; p0 < p1; p0 += U) {
-    uint4 x4[U];
+  const int p0 = part * per, p1 = min(n_pass, p0 + per);
+  if (p0 >= p1) return;
+  if (p0 < nq + nk) angles(__ldg(p.pos + t), p.inv_freq, p.rot / 2, p.mscale, lane, sc[warp]);
+
+  // rows sub, sub + RPW, .. of passes [i0, i1) of H heads: x -> y -> put
+  auto rows = [&](int i0, int i1, int H, const __nv_bfloat16* src, long long hs, const void* w, auto put) {
+    V8 C, S;
+    {
+      V8 c, s, wv;
+      own.read(sc[warp], c, s);
+      own.weights(w, p.w_f32, wv);
+      mul8(C, wv, c);
+      mul8(S, Lane<D, INTER>::swap(wv), s);
+    }
+    for (int i = i0; i < i1; i += U) {
+      uint2 xa[U], xb[U];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int row = (p0 + u) * RPW + sub;
-      x4[u] = make_uint4(0u, 0u, 0u, 0u);
-      if (p0 + u < p1 && row < p.rows) {
-        const __nv_bfloat16* src = row < p.Hq            ? p.q + t * p.q_ts + row * p.q_hs
-                                   : row < p.Hq + p.Hk ? p.k + t * p.k_ts + (row - p.Hq) * p.k_hs
-                                                       : p.v + t * p.v_ts + (row - p.Hq - p.Hk) * p.v_hs;
-        x4[u] = __ldg(reinterpret_cast<const uint4*>(src) + li);
+      for (int u = 0; u < U; ++u) {
+        const int h = (i + u) * RPW + sub;
+        xa[u] = xb[u] = make_uint2(0u, 0u);
+        if (i + u < i1 && h < H) {
+          xa[u] = __ldg(reinterpret_cast<const uint2*>(src + h * hs + own.a));
+          xb[u] = __ldg(reinterpret_cast<const uint2*>(src + h * hs + own.b));
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (i + u >= i1) break;  // (warp-uniform)
+        const int h = (i + u) * RPW + sub;
+        V8 x, y;
+        unpack4(xa[u], x.x);
+        unpack4(xb[u], x.x + 4);
+        mul8(y, x, C);
+        if (own.on) fma8(y, Lane<D, INTER>::swap(x), S, y);
+        if (w) scale8(y, y, rsqrtf(row_sum<LPR>(dot8(x, x)) * (1.f / D) + p.eps));
+        if (h < H) put(h, y);
       }
     }
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      if (p0 + u >= p1) break;  // (warp-uniform)
-      const int row = (p0 + u) * RPW + sub;
-      const bool is_q = row < p.Hq, is_k = !is_q && row < p.Hq + p.Hk;
-      float x[8];
-      unpack8(x4[u], x);
-      float y[8];
-      if (p.qw) {  // (both weights are given, or neither)
-        float ss = 0.f;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) ss += x[e] * x[e];
-        const float r = rsqrtf(row_sum<LPR>(ss) * (1.f / D) + p.eps);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) y[e] = x[e] * r * (is_q ? wq[e] : wk[e]);
-      } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) y[e] = x[e];
-      }
-      rot.apply(y, 1.f);
-      if (row >= p.rows) continue;
-      if (is_q) {
-        reinterpret_cast<uint4*>(p.q_out + ((long long)t * p.Hq + row) * D)[li] = pack8(y);
-      } else if (!PAGED) {
-        reinterpret_cast<uint4*>(p.k_out + ((long long)t * p.Hk + row - p.Hq) * D)[li] = pack8(y);
+  };
+  if (p0 < nq)
+    rows(p0, min(p1, nq), p.Hq, p.q + t * p.q_ts, p.q_hs, p.qw, [&](int h, const V8& y) {
+      __nv_bfloat16* dst = p.q_out + ((long long)t * p.Hq + h) * D;
+      *reinterpret_cast<uint2*>(dst + own.a) = pack4(y.x);
+      *reinterpret_cast<uint2*>(dst + own.b) = pack4(y.x + 4);
+    });
+  if (p1 > nq && p0 < nq + nk)
+    rows(max(p0, nq) - nq, min(p1, nq + nk) - nq, p.Hk, p.k + t * p.k_ts, p.k_hs, p.kw, [&](int h, V8& y) {
+      if (!PAGED) {
+        __nv_bfloat16* dst = p.k_out + ((long long)t * p.Hk + h) * D;
+        *reinterpret_cast<uint2*>(dst + own.a) = pack4(y.x);
+        *reinterpret_cast<uint2*>(dst + own.b) = pack4(y.x + 4);
       } else if (kc >= 0) {
-        const int h = is_k ? row - p.Hq : row - p.Hq - p.Hk;
-        const long long at = (is_k ? kc + h * p.kp_hs : vc + h * p.vp_hs) + li * 8;
-        void* pool = is_k ? p.k_pages : p.v_pages;
+        const long long at = kc + h * p.kp_hs;
         if (F8) {
-          const float inv = is_k ? p.k_inv : p.v_inv;
-#pragma unroll
-          for (int e = 0; e < 8; ++e) y[e] = (is_k ? y[e] : x[e]) * inv;
-          *reinterpret_cast<uint2*>((uint8_t*)pool + at) = pack8_e4m3(y);
+          scale8(y, y, p.k_inv);
+          *reinterpret_cast<uint32_t*>((uint8_t*)p.k_pages + at + own.a) = pack4_e4m3(y.x);
+          *reinterpret_cast<uint32_t*>((uint8_t*)p.k_pages + at + own.b) = pack4_e4m3(y.x + 4);
         } else {
-          *reinterpret_cast<uint4*>((__nv_bfloat16*)pool + at) = is_k ? pack8(y) : x4[u];
+          *reinterpret_cast<uint2*>((__nv_bfloat16*)p.k_pages + at + own.a) = pack4(y.x);
+          *reinterpret_cast<uint2*>((__nv_bfloat16*)p.k_pages + at + own.b) = pack4(y.x + 4);
         }
+      }
+    });
+  if (PAGED && vc >= 0) {  // the values as they are, 8 adjacent elements a lane
+    const int li8 = (lane % LPR) * 8;
+    for (int i = max(p0, nq + nk); i < p1; ++i) {
+      const int h = (i - nq - nk) * RPW + sub;
+      if (h >= p.Hk) continue;
+      const uint4 w = __ldg(reinterpret_cast<const uint4*>(p.v + t * p.v_ts + h * p.v_hs + li8));
+      const long long at = vc + h * p.vp_hs + li8;
+      if (F8) {
+        V8 x;
+        unpack4(make_uint2(w.x, w.y), x.x);
+        unpack4(make_uint2(w.z, w.w), x.x + 4);
+        scale8(x, x, p.v_inv);
+        *reinterpret_cast<uint2*>((uint8_t*)p.v_pages + at) = make_uint2(pack4_e4m3(x.x), pack4_e4m3(x.x + 4));
+      } else {
+        *reinterpret_cast<uint4*>((__nv_bfloat16*)p.v_pages + at) = w;
       }
     }
   }
@@ -246,103 +281,123 @@ __global__ void __launch_bounds__(NT) rope_fwd_kernel(Params p) {
 // in registers; a block adds its warps' in a fixed order and writes one record (rope_dw_kernel adds
 // the records, also in a fixed order: the result does not vary from run to run).
 template <int D, bool INTER, bool GK32>
-__global__ void __launch_bounds__(NT) rope_bwd_kernel(Params p) {
+__global__ void __launch_bounds__(NT, 3) rope_bwd_kernel(Params p) {
   constexpr int LPR = D / 8, RPW = 32 / LPR, U = 2;
   __shared__ float2 sc[NW][MAX_HALF];
   __shared__ float red[NW][2][D];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int li = lane % LPR, sub = lane / LPR;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = lane / LPR;
   griddep_wait();
   griddep_launch_dependents();
-  Rot<D, INTER> rot;
-  rot.init(lane, p.rot);
-  float wq[8], wk[8], aq[8], ak[8];
-  load_w8(p.qw, p.w_f32, li * 8, wq);
-  load_w8(p.kw, p.w_f32, li * 8, wk);
+  const Lane<D, INTER> own(lane, p.rot);
+  V8 aq, ak;  // weight gradients
 #pragma unroll
-  for (int e = 0; e < 8; ++e) aq[e] = ak[e] = 0.f;
-  const int n_pass = (p.rows + RPW - 1) / RPW;
+  for (int e = 0; e < 8; ++e) aq.x[e] = ak.x[e] = 0.f;
+  const int nq = (p.Hq + RPW - 1) / RPW, nk = (p.Hk + RPW - 1) / RPW, n_pass = nq + nk;  // passes
   const int per = (n_pass + p.parts - 1) / p.parts;
   const long long items = (long long)p.T * p.parts;
-  for (long long item = (long long)blockIdx.x * NW + warp; item < items; item += (long long)gridDim.x * NW) {
-    const int t = (int)(item / p.parts), part = (int)(item % p.parts);
-    const int p1 = min(n_pass, (part + 1) * per);
-    if (part * per >= p1) continue;
-    rot.angles(__ldg(p.pos + t), p.inv_freq, p.rot, p.mscale, lane, sc[warp]);
-    for (int p0 = part * per; p0 < p1; p0 += U) {
-      uint4 x4[U], g4[U], h4[U];
+
+  // passes [i0, i1) of H heads with the gradients g (bf16, or fp32) of [H, D]
+  auto rows = [&](int i0, int i1, int H, const __nv_bfloat16* src, long long hs, const void* w, const void* g, auto g32,
+                  __nv_bfloat16* dst, V8& acc) {
+    constexpr bool G32 = decltype(g32)::value;
+    V8 c, s, wv;
+    own.read(sc[warp], c, s);
+    own.weights(w, p.w_f32, wv);
+    for (int i = i0; i < i1; i += U) {
+      uint2 xa[U], xb[U];
+      uint4 ga[U], gb[U];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const int row = (p0 + u) * RPW + sub;
-        x4[u] = g4[u] = h4[u] = make_uint4(0u, 0u, 0u, 0u);
-        if (p0 + u < p1 && row < p.rows) {
-          if (row < p.Hq) {
-            if (p.qw) x4[u] = __ldg(reinterpret_cast<const uint4*>(p.q + t * p.q_ts + row * p.q_hs) + li);
-            g4[u] = __ldg(reinterpret_cast<const uint4*>(p.dq_out + ((long long)t * p.Hq + row) * D) + li);
+        const int h = (i + u) * RPW + sub;
+        xa[u] = xb[u] = make_uint2(0u, 0u);
+        ga[u] = gb[u] = make_uint4(0u, 0u, 0u, 0u);
+        if (i + u < i1 && h < H) {
+          if (w) {
+            xa[u] = __ldg(reinterpret_cast<const uint2*>(src + h * hs + own.a));
+            xb[u] = __ldg(reinterpret_cast<const uint2*>(src + h * hs + own.b));
+          }
+          if (G32) {
+            ga[u] = __ldg(reinterpret_cast<const uint4*>((const float*)g + (long long)h * D + own.a));
+            gb[u] = __ldg(reinterpret_cast<const uint4*>((const float*)g + (long long)h * D + own.b));
           } else {
-            const long long at = ((long long)t * p.Hk + row - p.Hq) * D;
-            if (p.qw) x4[u] = __ldg(reinterpret_cast<const uint4*>(p.k + t * p.k_ts + (row - p.Hq) * p.k_hs) + li);
-            if (GK32) {
-              g4[u] = __ldg(reinterpret_cast<const uint4*>((const float*)p.dk_out + at) + 2 * li);
-              h4[u] = __ldg(reinterpret_cast<const uint4*>((const float*)p.dk_out + at) + 2 * li + 1);
-            } else {
-              g4[u] = __ldg(reinterpret_cast<const uint4*>((const __nv_bfloat16*)p.dk_out + at) + li);
-            }
+            const uint2 va = __ldg(reinterpret_cast<const uint2*>((const __nv_bfloat16*)g + (long long)h * D + own.a));
+            const uint2 vb = __ldg(reinterpret_cast<const uint2*>((const __nv_bfloat16*)g + (long long)h * D + own.b));
+            ga[u].x = va.x; ga[u].y = va.y;
+            gb[u].x = vb.x; gb[u].y = vb.y;
           }
         }
       }
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        if (p0 + u >= p1) break;  // (warp-uniform)
-        const int row = (p0 + u) * RPW + sub;
-        const bool is_q = row < p.Hq;
-        float x[8], g[8];
-        unpack8(x4[u], x);
-        if (GK32 && !is_q) {
-          const uint32_t a[8] = {g4[u].x, g4[u].y, g4[u].z, g4[u].w, h4[u].x, h4[u].y, h4[u].z, h4[u].w};
+        if (i + u >= i1) break;  // (warp-uniform)
+        const int h = (i + u) * RPW + sub;
+        V8 x, y, n;
+        unpack4(xa[u], x.x);
+        unpack4(xb[u], x.x + 4);
+        if (G32) {
+          const uint32_t v[8] = {ga[u].x, ga[u].y, ga[u].z, ga[u].w, gb[u].x, gb[u].y, gb[u].z, gb[u].w};
 #pragma unroll
-          for (int e = 0; e < 8; ++e) g[e] = __uint_as_float(a[e]);
+          for (int e = 0; e < 8; ++e) y.x[e] = __uint_as_float(v[e]);
         } else {
-          unpack8(g4[u], g);
+          unpack4(make_uint2(ga[u].x, ga[u].y), y.x);
+          unpack4(make_uint2(gb[u].x, gb[u].y), y.x + 4);
         }
-        rot.apply(g, -1.f);
-        if (p.qw) {
-          float ss = 0.f, ux = 0.f;
+        // the transpose: n = y c - partner s, with each element's own s
+        mul8(n, y, c);
+        if (own.on) {
+          V8 ys;
+          mul8(ys, y, s);  // partner's s is this element's, negated: n_a gets + y_b s_b
+          const V8 t2 = Lane<D, INTER>::swap(ys);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            ss += x[e] * x[e];
-            ux += g[e] * (is_q ? wq[e] : wk[e]) * x[e];
-          }
-          const float r = rsqrtf(row_sum<LPR>(ss) * (1.f / D) + p.eps);
-          const float m = row_sum<LPR>(ux) * (1.f / D) * r * r;
+          for (int e = 0; e < 8; e += 2) fadd2(n.x[e], n.x[e + 1], n.x[e], n.x[e + 1], t2.x[e], t2.x[e + 1]);
+        }
+        if (w) {
+          V8 u8, gx;
+          mul8(u8, n, wv);
+          mul8(gx, n, x);
+          const float r = rsqrtf(row_sum<LPR>(dot8(x, x)) * (1.f / D) + p.eps);
+          const float m = row_sum<LPR>(dot8(u8, x)) * (1.f / D) * r * r * r;
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const float gw = g[e] * x[e] * r;
-            if (is_q) aq[e] += gw;
-            else ak[e] += gw;
-            g[e] = r * (g[e] * (is_q ? wq[e] : wk[e]) - x[e] * m);
+          for (int e = 0; e < 8; e += 2) {
+            ffma2(acc.x[e], acc.x[e + 1], gx.x[e], gx.x[e + 1], r, r, acc.x[e], acc.x[e + 1]);
+            fmul2(u8.x[e], u8.x[e + 1], u8.x[e], u8.x[e + 1], r, r);
+            ffma2(n.x[e], n.x[e + 1], x.x[e], x.x[e + 1], -m, -m, u8.x[e], u8.x[e + 1]);
           }
         }
-        if (row < p.rows) {
-          __nv_bfloat16* dst = is_q ? p.dq + ((long long)t * p.Hq + row) * D : p.dk + ((long long)t * p.Hk + row - p.Hq) * D;
-          reinterpret_cast<uint4*>(dst)[li] = pack8(g);
+        if (h < H) {
+          *reinterpret_cast<uint2*>(dst + (long long)h * D + own.a) = pack4(n.x);
+          *reinterpret_cast<uint2*>(dst + (long long)h * D + own.b) = pack4(n.x + 4);
         }
       }
     }
+  };
+  for (long long item = (long long)blockIdx.x * NW + warp; item < items; item += (long long)gridDim.x * NW) {
+    const int t = (int)(item / p.parts), part = (int)(item % p.parts);
+    const int p0 = part * per, p1 = min(n_pass, p0 + per);
+    if (p0 >= p1) continue;
+    angles(__ldg(p.pos + t), p.inv_freq, p.rot / 2, p.mscale, lane, sc[warp]);
+    if (p0 < nq)
+      rows(p0, min(p1, nq), p.Hq, p.q + t * p.q_ts, p.q_hs, p.qw, p.dq_out + (long long)t * p.Hq * D, std::false_type{},
+           p.dq + (long long)t * p.Hq * D, aq);
+    if (p1 > nq)
+      rows(max(p0, nq) - nq, p1 - nq, p.Hk, p.k + t * p.k_ts, p.k_hs, p.kw,
+           (const char*)p.dk_out + (long long)t * p.Hk * D * (GK32 ? 4 : 2), std::integral_constant<bool, GK32>{},
+           p.dk + (long long)t * p.Hk * D, ak);
   }
   if (!p.qw) return;
 #pragma unroll
   for (int o = LPR; o < 32; o <<= 1)
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      aq[e] += __shfl_xor_sync(0xffffffffu, aq[e], o);
-      ak[e] += __shfl_xor_sync(0xffffffffu, ak[e], o);
+      aq.x[e] += __shfl_xor_sync(0xffffffffu, aq.x[e], o);
+      ak.x[e] += __shfl_xor_sync(0xffffffffu, ak.x[e], o);
     }
   if (sub == 0) {
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      red[warp][0][li * 8 + e] = aq[e];
-      red[warp][1][li * 8 + e] = ak[e];
+      const int at = e < 4 ? own.a + e : own.b + e - 4;
+      red[warp][0][at] = aq.x[e];
+      red[warp][1][at] = ak.x[e];
     }
   }
   __syncthreads();
@@ -375,10 +430,14 @@ __global__ void __launch_bounds__(1024) rope_dw_kernel(const float* part, int n,
 }
 
 // -------------------------------------------------------------------------------------- host
+// Passes of a token: 256 / d rows at a time of the queries, and of the keys (and values) n times
+static int passes_of(int Hq, int Hk, int n, int d) {
+  const int rpw = 256 / d;
+  return (Hq + rpw - 1) / rpw + n * ((Hk + rpw - 1) / rpw);
+}
 // Warps that share a token: one when there are tokens enough to fill the GPU's warps (the angles are
 // computed once per token), else as many as it takes, down to one pass of rows a warp.
-static int parts_of(int T, int rows, int rpw, int sms) {
-  const int passes = (rows + rpw - 1) / rpw;
+static int parts_of(int T, int passes, int sms) {
   const long long want = ((long long)sms * 32 + T - 1) / T;
   return (int)(want < 1 ? 1 : want > passes ? passes : want);
 }
@@ -408,10 +467,10 @@ static cudaError_t launch_bwd(const Params& p, int grid, bool inter, bool gk32, 
 
 constexpr size_t kStatusBytes = 256;
 // Blocks of the backward: every warp of the GPU busy (the weight gradients are one record a block)
-static int bwd_grid(int T, int rows, int rpw, int sms, int& parts) {
-  parts = parts_of(T, rows, rpw, sms);
+static int bwd_grid(int T, int passes, int sms, int& parts) {
+  parts = parts_of(T, passes, sms);
   const long long blocks = ((long long)T * parts + NW - 1) / NW;
-  return (int)(blocks < sms * 4ll ? blocks : sms * 4ll);
+  return (int)(blocks < sms * 3ll ? blocks : sms * 3ll);
 }
 
 static bool strides_ok(const void* p, long long ts, long long hs) {
@@ -449,8 +508,8 @@ hs2_status hs2_qk_norm_rope(const hs2_bf16* Q, const hs2_bf16* K, long long q_to
   p.q_ts = q_token_stride; p.q_hs = q_head_stride; p.k_ts = k_token_stride; p.k_hs = k_head_stride;
   p.pos = positions; p.inv_freq = inv_freq;
   p.qw = q_weight; p.kw = k_weight ? k_weight : q_weight; p.w_f32 = weight_fp32;
-  p.T = T; p.Hq = Hq; p.Hk = Hk; p.rot = rot; p.rows = Hq + Hk;
-  p.parts = rope::parts_of(T, p.rows, 256 / d, num_sms());
+  p.T = T; p.Hq = Hq; p.Hk = Hk; p.rot = rot;
+  p.parts = rope::parts_of(T, rope::passes_of(Hq, Hk, 1, d), num_sms());
   p.eps = eps; p.mscale = mscale;
   p.q_out = (__nv_bfloat16*)q_out; p.k_out = (__nv_bfloat16*)k_out;
   const cudaError_t e = d == 128 ? rope::launch_fwd<128>(p, interleaved != 0, false, false, (cudaStream_t)stream)
@@ -487,8 +546,8 @@ hs2_status hs2_qk_norm_rope_paged(const hs2_bf16* Q, const hs2_bf16* K, const hs
   p.v_ts = v_token_stride; p.v_hs = v_head_stride;
   p.pos = positions; p.inv_freq = inv_freq; p.slots = slots;
   p.qw = q_weight; p.kw = k_weight; p.w_f32 = weight_fp32;
-  p.T = T; p.Hq = Hq; p.Hk = Hk; p.rot = rot; p.rows = Hq + 2 * Hk;
-  p.parts = rope::parts_of(T, p.rows, 256 / d, num_sms());
+  p.T = T; p.Hq = Hq; p.Hk = Hk; p.rot = rot;
+  p.parts = rope::parts_of(T, rope::passes_of(Hq, Hk, 2, d), num_sms());
   p.eps = eps; p.mscale = mscale;
   p.q_out = (__nv_bfloat16*)q_out; p.k_pages = k_pages; p.v_pages = v_pages;
   p.kp_ps = k_page_strides[0]; p.kp_rs = k_page_strides[1]; p.kp_hs = k_page_strides[2];
@@ -505,7 +564,7 @@ size_t hs2_qk_norm_rope_bwd_workspace_bytes(int T, int Hq, int Hk, int d) {
   if (!rope::sizes_ok(T, Hq, Hk) || (d != 64 && d != 128)) return 0;
   const int sms = num_sms() > 0 ? num_sms() : 148;
   int parts = 1;
-  const int grid = T > 0 ? rope::bwd_grid(T, Hq + Hk, 256 / d, sms, parts) : 0;
+  const int grid = T > 0 ? rope::bwd_grid(T, rope::passes_of(Hq, Hk, 1, d), sms, parts) : 0;
   return rope::kStatusBytes + (size_t)grid * 2 * d * sizeof(float);
 }
 
@@ -533,14 +592,14 @@ hs2_status hs2_qk_norm_rope_bwd(const hs2_bf16* Q, const hs2_bf16* K, long long 
   p.q_ts = q_token_stride; p.q_hs = q_head_stride; p.k_ts = k_token_stride; p.k_hs = k_head_stride;
   p.pos = positions; p.inv_freq = inv_freq;
   p.qw = q_weight; p.kw = k_weight ? k_weight : q_weight; p.w_f32 = weight_fp32;
-  p.T = T; p.Hq = Hq; p.Hk = Hk; p.rot = rot; p.rows = Hq + Hk;
+  p.T = T; p.Hq = Hq; p.Hk = Hk; p.rot = rot;
   p.eps = eps; p.mscale = mscale;
   p.dq_out = (const __nv_bfloat16*)dq_out; p.dk_out = dk_out;
   p.dq = (__nv_bfloat16*)dQ; p.dk = (__nv_bfloat16*)dK;
   p.part = (float*)((uint8_t*)workspace + rope::kStatusBytes);
   int grid = 0;
   if (T > 0) {
-    grid = rope::bwd_grid(T, p.rows, 256 / d, num_sms(), p.parts);
+    grid = rope::bwd_grid(T, rope::passes_of(Hq, Hk, 1, d), num_sms(), p.parts);
     const cudaError_t e = d == 128 ? rope::launch_bwd<128>(p, grid, interleaved != 0, dk_out_fp32 != 0, st)
                                    : rope::launch_bwd<64>(p, grid, interleaved != 0, dk_out_fp32 != 0, st);
     if (e != cudaSuccess) return HS2_ERR_CUDA;
