@@ -281,8 +281,8 @@ __global__ void __launch_bounds__(NT, 4) rope_fwd_kernel(Params p) {
 // in registers; a block adds its warps' in a fixed order and writes one record (rope_dw_kernel adds
 // the records, also in a fixed order: the result does not vary from run to run).
 template <int D, bool INTER, bool GK32>
-__global__ void __launch_bounds__(NT, 3) rope_bwd_kernel(Params p) {
-  constexpr int LPR = D / 8, RPW = 32 / LPR, U = 2;
+__global__ void __launch_bounds__(NT, 2) rope_bwd_kernel(Params p) {
+  constexpr int LPR = D / 8, RPW = 32 / LPR, U = 4;
   __shared__ float2 sc[NW][MAX_HALF];
   __shared__ float red[NW][2][D];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = lane / LPR;
@@ -470,7 +470,7 @@ constexpr size_t kStatusBytes = 256;
 static int bwd_grid(int T, int passes, int sms, int& parts) {
   parts = parts_of(T, passes, sms);
   const long long blocks = ((long long)T * parts + NW - 1) / NW;
-  return (int)(blocks < sms * 3ll ? blocks : sms * 3ll);
+  return (int)(blocks < sms * 2ll ? blocks : sms * 2ll);
 }
 
 static bool strides_ok(const void* p, long long ts, long long hs) {
