@@ -34,6 +34,7 @@ constexpr int NT = 192;   // TMA warp, MMA warp, four softmax warps
 constexpr int MH = 64;    // MMA rows
 constexpr int kNoPage = -2147483647 - 1;
 constexpr int MIN_TILES = 2;  // a CTA's share at least: a record costs about as much as a tile
+constexpr int OV = 2;         // what starting and ending a pair costs, in tiles
 
 struct Params {
   const __nv_bfloat16* q;  // [B, Hq, D]
@@ -124,22 +125,29 @@ __device__ __forceinline__ int seq_tiles(const Params& p, int b, int& len, int& 
   return len > 0 ? (len + TILE - 1) / TILE - t0 : 0;
 }
 
+// A pair's length on the line: its tiles and OV more in front of them, so that a CTA whose range holds many
+// short pairs gets fewer tiles.
+__device__ __forceinline__ int pair_len(int n) { return n > 0 ? n + OV : 0; }
+
 // The segments of a range [pos, end) of the line: runs of tiles of one (sequence, key head).
 template <int TILE>
 struct Walk {
-  int b, base, len, t0, n;  // the sequence, its first tile on the line, its length, first tile, tiles per head
+  int b, base, len, t0, n;  // the sequence, its start on the line, its length, first tile, tiles per head
   int pos, end;
   int hk, off, cnt;         // the segment: key head, first tile within the head's run, tiles
   __device__ __forceinline__ bool next(const Params& p) {
     while (pos < end) {
-      if (n > 0 && pos < base + p.Hk * n) {
-        hk = (pos - base) / n;
-        off = pos - base - hk * n;
-        cnt = min(n - off, end - pos);
-        pos += cnt;
-        return true;
+      const int m = pair_len(n);
+      if (m > 0 && pos < base + p.Hk * m) {
+        hk = (pos - base) / m;
+        const int x = pos - base - hk * m, y = min(m, x + end - pos);
+        pos += y - x;
+        off = max(x - OV, 0);
+        cnt = y - OV - off;
+        if (cnt > 0) return true;
+        continue;
       }
-      base += p.Hk * n;
+      base += p.Hk * m;
       ++b;
       if (b >= p.B) return false;
       n = seq_tiles<TILE>(p, b, len, t0);
@@ -151,12 +159,21 @@ struct Walk {
   }
 };
 
-__device__ __forceinline__ int range_start(int w, int N, int W) { return (int)((long long)w * N / W); }
-// CTAs that share N tiles
-__device__ __forceinline__ int used_ctas(int N, int W) {
-  const int most = (N + MIN_TILES - 1) / MIN_TILES;
-  return most < W ? (most > 0 ? most : 1) : W;
-}
+// The ranges of N tiles: the first N % W CTAs take one tile more than the others (one 32-bit division; a
+// 64-bit w N / W cost the join as much as its records).
+struct Split {
+  int W, q, r;
+  __device__ __forceinline__ Split(int N, int most) {
+    W = min(most, max((N + MIN_TILES - 1) / MIN_TILES, 1));
+    q = N / W;
+    r = N - q * W;
+  }
+  __device__ __forceinline__ int start(int w) const { return w * q + min(w, r); }
+  __device__ __forceinline__ int owner(int tile) const {  // the CTA whose range holds it
+    const int cut = r * (q + 1);
+    return tile < cut ? tile / (q + 1) : r + (tile - cut) / q;
+  }
+};
 
 template <int D, bool F8>
 __global__ void __launch_bounds__(NT, 2) paged_attn_kernel(const __grid_constant__ CUtensorMap tmK,
@@ -198,7 +215,7 @@ __global__ void __launch_bounds__(NT, 2) paged_attn_kernel(const __grid_constant
   for (int i = 0; i < per; ++i) {
     const int b = tid * per + i;
     int len, t0;
-    if (b < p.B) mine += seq_tiles<TILE>(p, b, len, t0, &bad);
+    if (b < p.B) mine += pair_len(seq_tiles<TILE>(p, b, len, t0, &bad));
   }
   int x = mine;
 #pragma unroll
@@ -217,14 +234,15 @@ __global__ void __launch_bounds__(NT, 2) paged_attn_kernel(const __grid_constant
     if (w < warp) before += s;
     all += s;
   }
-  const int N = all * p.Hk, W = used_ctas(N, p.W), cta = blockIdx.x;
-  const int r0 = cta < W ? range_start(cta, N, W) : N, r1 = cta < W ? range_start(cta + 1, N, W) : N;
+  const int N = all * p.Hk, cta = blockIdx.x;
+  const Split split(N, p.W);
+  const int r0 = cta < split.W ? split.start(cta) : N, r1 = cta < split.W ? split.start(cta + 1) : N;
   if (r0 < r1 && before * p.Hk <= r0 && r0 < (before + mine) * p.Hk) {
     int at = before * p.Hk;
     for (int i = 0; i < per; ++i) {
       const int b = tid * per + i;
       int len, t0;
-      const int n = seq_tiles<TILE>(p, b, len, t0);
+      const int n = pair_len(seq_tiles<TILE>(p, b, len, t0));
       if (r0 < at + n * p.Hk) {
         s_start[0] = b; s_start[1] = at; s_start[2] = len; s_start[3] = t0;
         break;
@@ -239,7 +257,7 @@ __global__ void __launch_bounds__(NT, 2) paged_attn_kernel(const __grid_constant
       int len, t0;
       if (b < p.B) {
         p.pre[b] = at;
-        at += seq_tiles<TILE>(p, b, len, t0) * p.Hk;
+        at += pair_len(seq_tiles<TILE>(p, b, len, t0)) * p.Hk;
       }
     }
     if (tid == 0) p.pre[p.B] = N;
@@ -386,144 +404,152 @@ __global__ void __launch_bounds__(NT, 2) paged_attn_kernel(const __grid_constant
     // warp quarter qd share head row 16 qd + l (TMEM keeps the rows of an M = 64 accumulator in the
     // first 16 lanes of each quarter); the first takes a tile's lower keys and the head's lower
     // columns, the second the upper ones
-    const int qd = warp & 3, row = qd * 16 + (lane & 15), half = lane >> 4;
+    const int qd = warp & 3, row = qd * 16 + (lane & 15), lh = lane >> 4;
     const uint32_t tq = tmem + ((uint32_t)(qd * 32) << 16);
-    const int stid = qd * 32 + lane;
-    constexpr int NL = TILE / 64;  // 32-column loads of S per lane
-    constexpr int NO = D / 64;     // ... of O
+    constexpr int SC = TILE / 2, OC = D / 2;  // columns of a lane
+    constexpr int NL = SC / 32, NO = OC / 32;
+    const int s0 = lh * SC, o0 = lh * OC;     // the first ones
     uint32_t js = 0, jp = 0, ring = 0;
     bool ok = true;
-    while (ok && wk.next(p)) {
-      // ---- this head's query row -> shared memory
+    // a pair's query row -> shared memory (once its last pair's score products are done); the
+    // factor from its scores to exponents
+    auto load_q = [&](int pair) -> float {
       float c = p.c;
-      {
-        const __nv_bfloat16* src = p.q + ((size_t)(wk.b * p.Hk + wk.hk) * p.G + row) * D + half * (D / 2);
+      const __nv_bfloat16* src = p.q + ((size_t)pair * p.G + row) * D;
+      if constexpr (F8) {
         uint4 w[D / 16];
 #pragma unroll
         for (int i = 0; i < D / 16; ++i)
-          w[i] = row < p.G ? __ldg(reinterpret_cast<const uint4*>(src) + i) : make_uint4(0u, 0u, 0u, 0u);
-        if constexpr (F8) {
-          float am = 0.f, nan = 0.f;
+          w[i] = row < p.G ? __ldg(reinterpret_cast<const uint4*>(src + o0) + i) : make_uint4(0u, 0u, 0u, 0u);
+        float am = 0.f, nan = 0.f;
 #pragma unroll
-          for (int i = 0; i < D / 16; ++i) {
-            const uint32_t a[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+        for (int i = 0; i < D / 16; ++i) {
+          const uint32_t a[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const float v0 = __uint_as_float(a[k] << 16), v1 = __uint_as_float(a[k] & 0xFFFF0000u);
-              am = fmaxf(am, fmaxf(fabsf(v0), fabsf(v1)));
-              nan += (v0 - v0) + (v1 - v1);  // NaN when an element is infinite or NaN
-            }
-          }
-          am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, 16));
-          nan += __shfl_xor_sync(0xffffffffu, nan, 16);
-          // am 2^e in [128, 256)
-          int e = 134 - (int)(__float_as_uint(am) >> 23);  // 127 + 7 - biased exponent
-          e = am > 0.f ? (e < -120 ? -120 : e > 120 ? 120 : e) : 0;
-          const float up = __uint_as_float((uint32_t)(127 + e) << 23);
-          c = p.c * __uint_as_float((uint32_t)(127 - e) << 23) + nan;
-#pragma unroll
-          for (int i = 0; i < D / 16; i += 2) {
-            uint32_t hi[4], lo[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const uint4& ww = w[i + k / 2];
-              const uint32_t a = k % 2 ? ww.z : ww.x, b2 = k % 2 ? ww.w : ww.y;
-              uint32_t h0, l0, h1, l1;
-              // (a bf16 element times a power of two below 256 is an f16 value, or too small to matter)
-              split_e4m3(pack_f16x2(__uint_as_float(a << 16) * up, __uint_as_float(a & 0xFFFF0000u) * up), h0, l0);
-              split_e4m3(pack_f16x2(__uint_as_float(b2 << 16) * up, __uint_as_float(b2 & 0xFFFF0000u) * up), h1, l1);
-              hi[k] = h0 | (h1 << 16);
-              lo[k] = l0 | (l1 << 16);
-            }
-            const uint32_t dst = smem_u32(sQ) + sw128_off(row, half * (D / 32) + i / 2);
-            st_shared_v4(dst, hi[0], hi[1], hi[2], hi[3]);
-            st_shared_v4(dst + MH * 128, lo[0], lo[1], lo[2], lo[3]);
-          }
-        } else {
-#pragma unroll
-          for (int i = 0; i < D / 16; ++i) {
-            const int ch = half * (D / 16) + i;
-            st_shared_v4(smem_u32(sQ) + (ch / 8) * (MH * 128) + sw128_off(row, ch % 8), w[i].x, w[i].y, w[i].z, w[i].w);
+          for (int k = 0; k < 4; ++k) {
+            const float v0 = __uint_as_float(a[k] << 16), v1 = __uint_as_float(a[k] & 0xFFFF0000u);
+            am = fmaxf(am, fmaxf(fabsf(v0), fabsf(v1)));
+            nan += (v0 - v0) + (v1 - v1);  // NaN when an element is infinite or NaN
           }
         }
-        fence_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&q_ready);
+        am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, 16));
+        nan += __shfl_xor_sync(0xffffffffu, nan, 16);
+        // am 2^e in [128, 256)
+        int e = 134 - (int)(__float_as_uint(am) >> 23);  // 127 + 7 - biased exponent
+        e = am > 0.f ? (e < -120 ? -120 : e > 120 ? 120 : e) : 0;
+        const float up = __uint_as_float((uint32_t)(127 + e) << 23);
+        c = p.c * __uint_as_float((uint32_t)(127 - e) << 23) + nan;
+#pragma unroll
+        for (int i = 0; i < D / 16; i += 2) {
+          uint32_t hi[4], lo[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const uint4& ww = w[i + k / 2];
+            const uint32_t a = k % 2 ? ww.z : ww.x, b2 = k % 2 ? ww.w : ww.y;
+            uint32_t h0, l0, h1, l1;
+            // (a bf16 element times a power of two below 256 is an f16 value, or too small to matter)
+            split_e4m3(pack_f16x2(__uint_as_float(a << 16) * up, __uint_as_float(a & 0xFFFF0000u) * up), h0, l0);
+            split_e4m3(pack_f16x2(__uint_as_float(b2 << 16) * up, __uint_as_float(b2 & 0xFFFF0000u) * up), h1, l1);
+            hi[k] = h0 | (h1 << 16);
+            lo[k] = l0 | (l1 << 16);
+          }
+          const uint32_t dst = smem_u32(sQ) + sw128_off(row, o0 / 16 + i / 2);
+          st_shared_v4(dst, hi[0], hi[1], hi[2], hi[3]);
+          st_shared_v4(dst + MH * 128, lo[0], lo[1], lo[2], lo[3]);
+        }
+      } else {
+        uint4 w[OC / 8];
+#pragma unroll
+        for (int i = 0; i < OC / 8; ++i)
+          w[i] = row < p.G ? __ldg(reinterpret_cast<const uint4*>(src + o0) + i) : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+        for (int i = 0; i < OC / 8; ++i) {
+          const int ch = o0 / 8 + i;
+          st_shared_v4(smem_u32(sQ) + (ch / 8) * (MH * 128) + sw128_off(row, ch % 8), w[i].x, w[i].y, w[i].z, w[i].w);
+        }
       }
+      fence_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&q_ready);
+      return c;
+    };
+    bool more = wk.next(p);
+    float c = more ? load_q(wk.b * p.Hk + wk.hk) : 0.f;
+    while (more) {
       float m_run = -INFINITY, l_run = 0.f, al = 1.f, be = 0.f;  // al, be: factors of the last tile's O
-      float acc[NO][32];
+      float acc[OC];
 #pragma unroll
-      for (int i = 0; i < NO; ++i)
-#pragma unroll
-        for (int k = 0; k < 32; ++k) acc[i][k] = 0.f;
+      for (int k = 0; k < OC; ++k) acc[k] = 0.f;
       // acc = acc al + O be for the tile whose PV was issued last
       auto add_o = [&]() -> bool {
         if (!warp_wait(&o_full, jp & 1, limit, &abort_flag, p.st, 721)) return false;
         ++jp;
         tc_fence_after();
+        const bool grown = __any_sync(0xffffffffu, al != 1.f);  // a row's maximum moved: rare after its first tiles
 #pragma unroll
-        for (int i = 0; i < NO; ++i) {
+        for (int j = 0; j < NO; ++j) {
           float o[32];
-          tmem_ld16x2_32<D / 2>(tq + tO + i * 32, o);
+          tmem_ld16x2_32<OC>(tq + tO + j * 32, o);
           tmem_ld_wait();
 #pragma unroll
-          for (int k = 0; k < 32; ++k) acc[i][k] = acc[i][k] * al + o[k] * be;
+          for (int k = 0; k < 32; k += 2) {
+            float &x = acc[j * 32 + k], &y = acc[j * 32 + k + 1];
+            if (grown) fmul2(x, y, x, y, al, al);
+            ffma2(x, y, o[k], o[k + 1], be, be, x, y);
+          }
         }
         tc_fence_before();
         return true;
       };
-      const int first = wk.first_key(p);
-      const int t_lo = wk.t0 + wk.off;
-      for (int i = 0; i < wk.cnt && ok; ++i) {
+      const int first = wk.first_key(p), len = wk.len, cnt = wk.cnt, t_lo = wk.t0 + wk.off;
+      const int pair = wk.b * p.Hk + wk.hk;
+      const bool whole = wk.cnt == wk.n, begins = wk.off == 0;
+      for (int i = 0; i < cnt; ++i) {
         const int key0 = (t_lo + i) * TILE;
-        const int lo = max(first - key0, 0), hi = min(wk.len - key0, TILE);  // visible keys of the tile
+        const int lo = max(first - key0, 0), hi = min(len - key0, TILE);  // visible keys of the tile
         if (!warp_wait(&s_full, js & 1, limit, &abort_flag, p.st, 720)) { ok = false; break; }
         ++js;
+        float sv[SC];
         tc_fence_after();
-        float sv[NL][32];
 #pragma unroll
-        for (int j = 0; j < NL; ++j) tmem_ld16x2_32<TILE / 2>(tq + tS + j * 32, sv[j]);
+        for (int j = 0; j < NL; ++j) tmem_ld16x2_32<SC>(tq + tS + j * 32, *reinterpret_cast<float(*)[32]>(sv + j * 32));
         tmem_ld_wait();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&s_free);
         if (lo > 0 || hi < TILE) {
-          const int a = lo - half * (TILE / 2), b2 = hi - half * (TILE / 2);
+          const int a = lo - s0, b2 = hi - s0;
 #pragma unroll
-          for (int j = 0; j < NL; ++j)
-#pragma unroll
-            for (int k = 0; k < 32; ++k) sv[j][k] = j * 32 + k >= a && j * 32 + k < b2 ? sv[j][k] : -INFINITY;
+          for (int k = 0; k < SC; ++k) sv[k] = k >= a && k < b2 ? sv[k] : -INFINITY;
         }
-        float rm = max32(sv[0]);
+        float rm = fmaxf(sv[0], sv[1]);
 #pragma unroll
-        for (int j = 1; j < NL; ++j) rm = fmaxf(rm, max32(sv[j]));
+        for (int k = 2; k < SC; k += 2) rm = fmaxf(rm, fmaxf(sv[k], sv[k + 1]));
         rm = fmaxf(rm, __shfl_xor_sync(0xffffffffu, rm, 16));
         const float mt = rm * c;
         const float neg = mt == -INFINITY ? 0.f : F8 ? 8.f - mt : -mt;
         float la = 0.f, lb = 0.f;
-        uint32_t pk[NL * 16];  // bf16 pairs; e4m3: the hi codes of four keys, then the lo codes
+        uint32_t pk[SC / 2];  // bf16 pairs; e4m3: the hi codes of four keys, then the lo codes
 #pragma unroll
-        for (int j = 0; j < NL; ++j)
+        for (int k = 0; k < SC; k += 4) {
+          float e[4];
+          ffma2(e[0], e[1], sv[k], sv[k + 1], c, c, neg, neg);
+          ffma2(e[2], e[3], sv[k + 2], sv[k + 3], c, c, neg, neg);
 #pragma unroll
-          for (int k = 0; k < 32; k += 4) {
-            float e[4];
-            ffma2(e[0], e[1], sv[j][k], sv[j][k + 1], c, c, neg, neg);
-            ffma2(e[2], e[3], sv[j][k + 2], sv[j][k + 3], c, c, neg, neg);
-#pragma unroll
-            for (int y = 0; y < 4; ++y) e[y] = fast_exp2(e[y]);
-            fadd2(la, lb, la, lb, e[0], e[1]);
-            fadd2(la, lb, la, lb, e[2], e[3]);
-            if constexpr (F8) {
-              uint32_t h0, l0, h1, l1;
-              split_e4m3(pack_f16x2(e[0], e[1]), h0, l0);
-              split_e4m3(pack_f16x2(e[2], e[3]), h1, l1);
-              pk[j * 8 + k / 4] = h0 | (h1 << 16);
-              pk[NL * 8 + j * 8 + k / 4] = l0 | (l1 << 16);
-            } else {
-              pk[j * 16 + k / 2] = pack_bf16x2(e[0], e[1]);
-              pk[j * 16 + k / 2 + 1] = pack_bf16x2(e[2], e[3]);
-            }
+          for (int y = 0; y < 4; ++y) e[y] = fast_exp2(e[y]);
+          fadd2(la, lb, la, lb, e[0], e[1]);
+          fadd2(la, lb, la, lb, e[2], e[3]);
+          if constexpr (F8) {
+            uint32_t h0, l0, h1, l1;
+            split_e4m3(pack_f16x2(e[0], e[1]), h0, l0);
+            split_e4m3(pack_f16x2(e[2], e[3]), h1, l1);
+            pk[k / 4] = h0 | (h1 << 16);
+            pk[SC / 4 + k / 4] = l0 | (l1 << 16);
+          } else {
+            pk[k / 2] = pack_bf16x2(e[0], e[1]);
+            pk[k / 2 + 1] = pack_bf16x2(e[2], e[3]);
           }
+        }
         // the last tile's product before P is overwritten
         if (i > 0 && !add_o()) { ok = false; break; }
         // factors of this tile's product
@@ -535,26 +561,26 @@ __global__ void __launch_bounds__(NT, 2) paged_attn_kernel(const __grid_constant
         // ---- P -> shared memory, K-major
         if constexpr (F8) {
 #pragma unroll
-          for (int y = 0; y < NL * 2; ++y) {
-            const uint32_t dst = smem_u32(sP) + sw128_off(row, half * (NL * 2) + y);
+          for (int y = 0; y < SC / 16; ++y) {
+            const uint32_t dst = smem_u32(sP) + sw128_off(row, s0 / 16 + y);
             st_shared_v4(dst, pk[4 * y], pk[4 * y + 1], pk[4 * y + 2], pk[4 * y + 3]);
-            st_shared_v4(dst + MH * 128, pk[NL * 8 + 4 * y], pk[NL * 8 + 4 * y + 1], pk[NL * 8 + 4 * y + 2],
-                         pk[NL * 8 + 4 * y + 3]);
+            st_shared_v4(dst + MH * 128, pk[SC / 4 + 4 * y], pk[SC / 4 + 4 * y + 1], pk[SC / 4 + 4 * y + 2],
+                         pk[SC / 4 + 4 * y + 3]);
           }
         } else {
 #pragma unroll
-          for (int y = 0; y < NL * 4; ++y) {
-            const int ch = half * (NL * 4) + y;
+          for (int y = 0; y < SC / 8; ++y) {
+            const int ch = s0 / 8 + y;
             st_shared_v4(smem_u32(sP) + (ch / 8) * (MH * 128) + sw128_off(row, ch % 8), pk[4 * y], pk[4 * y + 1],
                          pk[4 * y + 2], pk[4 * y + 3]);
           }
         }
         if (lo > 0 || hi < TILE) {
           // rows of V that no key is in may hold anything, and 0 times an infinity or a NaN is not 0
-          const uint32_t vi = ring + (i == wk.cnt - 1 ? 2 * wk.cnt - 1 : 2 * i + 2);
+          const uint32_t vi = ring + (i == cnt - 1 ? 2 * cnt - 1 : 2 * i + 2);
           if (!warp_wait(&r_full[vi % NR], (vi / NR) & 1, limit, &abort_flag, p.st, 722)) { ok = false; break; }
           const uint32_t v = smem_u32(sR + (vi % NR) * SLOT);
-          for (int ch = stid; ch < SLOT / 16; ch += nact * 32) {
+          for (int ch = qd * 32 + lane; ch < SLOT / 16; ch += nact * 32) {
             const int r = (ch / 8) % TILE;
             if (r < lo || r >= hi) st_shared_v4(v + ch * 16, 0u, 0u, 0u, 0u);
           }
@@ -563,33 +589,31 @@ __global__ void __launch_bounds__(NT, 2) paged_attn_kernel(const __grid_constant
         __syncwarp();
         if (lane == 0) mbar_arrive(&p_ready);
       }
-      ring += 2 * wk.cnt;
-      if (!ok || !add_o()) { ok = false; break; }
+      if (!ok) break;
+      ring += 2 * cnt;
+      // the next pair's queries while the last product runs (its score products are done)
+      more = wk.next(p);
+      const float c_next = more ? load_q(wk.b * p.Hk + wk.hk) : 0.f;
+      if (!add_o()) break;
       l_run += __shfl_xor_sync(0xffffffffu, l_run, 16);
-      const size_t head = (size_t)(wk.b * p.Hk + wk.hk) * p.G + row;
-      if (row < p.G && wk.cnt == wk.n) {  // the whole row
+      if (row < p.G && whole) {
+        const size_t head = (size_t)pair * p.G + row;
         const float inv = l_run == 0.f ? 0.f : p.oscale / l_run;
-        uint4* dst = reinterpret_cast<uint4*>(p.out + head * D + half * (D / 2));
+        uint4* dst = reinterpret_cast<uint4*>(p.out + head * D + o0);
 #pragma unroll
-        for (int i = 0; i < NO; ++i)
+        for (int k = 0; k < OC; k += 8)
+          dst[k / 8] = make_uint4(pack_bf16x2(acc[k] * inv, acc[k + 1] * inv), pack_bf16x2(acc[k + 2] * inv, acc[k + 3] * inv),
+                                  pack_bf16x2(acc[k + 4] * inv, acc[k + 5] * inv),
+                                  pack_bf16x2(acc[k + 6] * inv, acc[k + 7] * inv));
+        if (p.lse && lh == 0) p.lse[head] = (m_run + log2f(l_run)) * 0.69314718055994531f;
+      } else if (row < p.G) {  // a record: slot 1 where the segment begins its pair, else slot 0
+        const size_t rec = ((size_t)cta * 2 + (begins ? 1 : 0)) * p.G + row;
+        float4* dst = reinterpret_cast<float4*>(p.po + rec * D + o0);
 #pragma unroll
-          for (int k = 0; k < 32; k += 8)
-            dst[i * 4 + k / 8] = make_uint4(pack_bf16x2(acc[i][k] * inv, acc[i][k + 1] * inv),
-                                            pack_bf16x2(acc[i][k + 2] * inv, acc[i][k + 3] * inv),
-                                            pack_bf16x2(acc[i][k + 4] * inv, acc[i][k + 5] * inv),
-                                            pack_bf16x2(acc[i][k + 6] * inv, acc[i][k + 7] * inv));
-        if (p.lse && half == 0) p.lse[head] = (m_run + log2f(l_run)) * 0.69314718055994531f;
-      } else if (row < p.G) {  // a record: slot 0 where the segment starts the CTA's range, else slot 1 (it ends it)
-        const int at = wk.base + wk.hk * wk.n + wk.off;
-        const size_t rec = ((size_t)cta * 2 + (at == r0 ? 0 : 1)) * p.G + row;
-        float4* dst = reinterpret_cast<float4*>(p.po + rec * D + half * (D / 2));
-#pragma unroll
-        for (int i = 0; i < NO; ++i)
-#pragma unroll
-          for (int k = 0; k < 32; k += 4)
-            dst[i * 8 + k / 4] = make_float4(acc[i][k], acc[i][k + 1], acc[i][k + 2], acc[i][k + 3]);
-        if (half == 0) p.pml[rec] = make_float2(m_run, l_run);
+        for (int k = 0; k < OC; k += 4) dst[k / 4] = make_float4(acc[k], acc[k + 1], acc[k + 2], acc[k + 3]);
+        if (lh == 0) p.pml[rec] = make_float2(m_run, l_run);
       }
+      c = c_next;
       __syncwarp();
     }
   }
@@ -599,70 +623,100 @@ __global__ void __launch_bounds__(NT, 2) paged_attn_kernel(const __grid_constant
 }
 
 // Joins the records of the (sequence, key head) pairs that several CTAs worked on, in the order of
-// their ranges, and writes the rows of sequences without a key. One warp per head row.
-constexpr int JT = 256;
+// their ranges, and writes the rows of sequences without a key. A pair cut into cnt segments has
+// cnt - 1 cuts inside it, and the block of each such cut joins every (cnt - 1)th of its head rows: all
+// blocks have about G records to read, however the line is cut (a block per head row left 1 MB a block
+// to read when eight long sequences share the GPU). A row's records are spread over the warps that the block
+// has to spare.
+constexpr int JT = 256, JW = JT / 32;
 template <int D>
 __global__ void __launch_bounds__(JT) paged_join_kernel(Params p) {
-  const int lane = threadIdx.x & 31, row = blockIdx.y * (JT / 32) + (threadIdx.x >> 5);
-  const int b = blockIdx.x / p.Hk, hk = blockIdx.x % p.Hk;
+  constexpr int VL = D / 32;  // columns of a lane
+  __shared__ float s_acc[JW][D], s_l[JW];
+  __shared__ int s_b, s_base, s_len;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, cut = blockIdx.x + 1;
   griddep_wait();
   griddep_launch_dependents();
-  if (row >= p.G) return;
-  const size_t head = (size_t)blockIdx.x * p.G + row;
-  const int base = __ldcg(p.pre + b), n = (__ldcg(p.pre + b + 1) - base) / p.Hk, N = __ldcg(p.pre + p.B);
-  constexpr int VL = D / 32;  // columns of a lane
-  __nv_bfloat16* dst = p.out + head * D + lane * VL;
-  if (n == 0) {
-#pragma unroll
-    for (int i = 0; i < VL; i += 2) *reinterpret_cast<uint32_t*>(dst + i) = 0u;
-    if (lane == 0 && p.lse) p.lse[head] = -INFINITY;
-    return;
-  }
-  const int W = used_ctas(N, p.W), s = base + hk * n, e = s + n;
-  int w0 = (int)((long long)s * W / N);  // the CTA whose range holds tile s
-  while (w0 > 0 && range_start(w0, N, W) > s) --w0;
-  while (range_start(w0 + 1, N, W) <= s) ++w0;
-  if (range_start(w0 + 1, N, W) >= e) return;  // finished by that CTA
-  int w1 = w0 + 1;  // past the last one
-  while (range_start(w1, N, W) < e) ++w1;
-  const int cnt = w1 - w0;
-  // only the first can start before tile s (then its record is the second one of that CTA)
-  const int first_slot = range_start(w0, N, W) == s ? 0 : 1;
-  auto rec = [&](int i) { return ((size_t)(w0 + i) * 2 + (i == 0 ? first_slot : 0)) * p.G + row; };
-  float M = -INFINITY;
-  for (int i = lane; i < cnt; i += 32) M = fmaxf(M, __ldcg(&p.pml[rec(i)]).x);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-  float acc[VL], l = 0.f;
-#pragma unroll
-  for (int i = 0; i < VL; ++i) acc[i] = 0.f;
-  for (int i0 = 0; i0 < cnt; i0 += 32) {
-    float w = 0.f;
-    if (i0 + lane < cnt) {
-      const float2 ml = __ldcg(&p.pml[rec(i0 + lane)]);
-      w = ml.x == -INFINITY ? 0.f : fast_exp2(ml.x - M);
-      l += ml.y * w;
+  const int N = __ldcg(p.pre + p.B);
+  const Split line(N, p.W);
+  const int at = cut < line.W ? line.start(cut) : N;
+  for (int b = tid; b < p.B; b += JT) {
+    const int x = __ldcg(p.pre + b), y = __ldcg(p.pre + b + 1);
+    if (x <= at && at < y) { s_b = b; s_base = x; s_len = y - x; }
+    if (x == y && b % gridDim.x == blockIdx.x) {
+      uint4* dst = reinterpret_cast<uint4*>(p.out + (size_t)b * p.Hk * p.G * D);
+      for (int i = 0; i < p.Hk * p.G * D / 8; ++i) dst[i] = make_uint4(0u, 0u, 0u, 0u);
+      if (p.lse)
+        for (int i = 0; i < p.Hk * p.G; ++i) p.lse[(size_t)b * p.Hk * p.G + i] = -INFINITY;
     }
-    const int m = min(32, cnt - i0);
+  }
+  if (cut >= line.W) return;
+  __syncthreads();
+  const int b = s_b, base = s_base, n = s_len / p.Hk, hk = (at - base) / n;
+  const int s = base + hk * n + OV, e = s + n - OV;
+  if (at <= s) return;  // not between two tiles of a pair
+  const int w0 = line.owner(s), w1 = line.owner(e - 1) + 1;
+  const int cnt = w1 - w0, first = cut - w0 - 1;  // first < cnt - 1
+  const int rows = first < p.G ? (p.G - first + cnt - 2) / (cnt - 1) : 0;
+  const int split = rows >= 8 ? 1 : rows >= 4 ? 2 : rows >= 2 ? 4 : 8, sub = warp % split;
+  for (int k0 = 0; k0 < rows; k0 += JW / split) {
+    const int k = k0 + warp / split, row = first + k * (cnt - 1);
+    const bool on = k < rows;
+    auto rec = [&](int i) { return ((size_t)(w0 + i) * 2 + (i == 0 ? 1 : 0)) * p.G + row; };
+    float M = -INFINITY, acc[VL], l = 0.f;
+#pragma unroll
+    for (int i = 0; i < VL; ++i) acc[i] = 0.f;
+    if (on) {
+      for (int i = lane; i < cnt; i += 32) M = fmaxf(M, __ldcg(&p.pml[rec(i)]).x);
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+      const int mine = (cnt - sub + split - 1) / split;  // records sub, sub + split, ..
+      for (int i0 = 0; i0 < mine; i0 += 32) {
+        float w = 0.f;
+        if (i0 + lane < mine) {
+          const float2 ml = __ldcg(&p.pml[rec(sub + (i0 + lane) * split)]);
+          w = ml.x == -INFINITY ? 0.f : fast_exp2(ml.x - M);
+          l += ml.y * w;
+        }
+        const int m = min(32, mine - i0);
 #pragma unroll 8
-    for (int i = 0; i < m; ++i) {
-      const float wi = __shfl_sync(0xffffffffu, w, i);
-      const float* src = p.po + rec(i0 + i) * D + lane * VL;
-      if constexpr (VL == 4) {
-        const float4 o = __ldcg(reinterpret_cast<const float4*>(src));
-        acc[0] += o.x * wi; acc[1] += o.y * wi; acc[2] += o.z * wi; acc[3] += o.w * wi;
-      } else {
-        const float2 o = __ldcg(reinterpret_cast<const float2*>(src));
-        acc[0] += o.x * wi; acc[1] += o.y * wi;
+        for (int i = 0; i < m; ++i) {
+          const float wi = __shfl_sync(0xffffffffu, w, i);
+          const float* src = p.po + rec(sub + (i0 + i) * split) * D + lane * VL;
+          if constexpr (VL == 4) {
+            const float4 o = __ldcg(reinterpret_cast<const float4*>(src));
+            acc[0] += o.x * wi; acc[1] += o.y * wi; acc[2] += o.z * wi; acc[3] += o.w * wi;
+          } else {
+            const float2 o = __ldcg(reinterpret_cast<const float2*>(src));
+            acc[0] += o.x * wi; acc[1] += o.y * wi;
+          }
+        }
       }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+    }
+    if (split > 1) {
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < VL; ++i) s_acc[warp][lane * VL + i] = acc[i];
+      if (lane == 0) s_l[warp] = l;
+      __syncthreads();
+      if (sub == 0)
+        for (int j = 1; j < split; ++j) {
+#pragma unroll
+          for (int i = 0; i < VL; ++i) acc[i] += s_acc[warp + j][lane * VL + i];
+          l += s_l[warp + j];
+        }
+    }
+    if (on && sub == 0) {
+      const size_t head = (size_t)(b * p.Hk + hk) * p.G + row;
+      const float inv = l == 0.f ? 0.f : p.oscale / l;
+      uint32_t* dst = reinterpret_cast<uint32_t*>(p.out + head * D + lane * VL);
+#pragma unroll
+      for (int i = 0; i < VL; i += 2) dst[i / 2] = pack_bf16x2(acc[i] * inv, acc[i + 1] * inv);
+      if (lane == 0 && p.lse) p.lse[head] = (M + log2f(l)) * 0.69314718055994531f;
     }
   }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-  const float inv = l == 0.f ? 0.f : p.oscale / l;
-#pragma unroll
-  for (int i = 0; i < VL; i += 2) *reinterpret_cast<uint32_t*>(dst + i) = pack_bf16x2(acc[i] * inv, acc[i + 1] * inv);
-  if (lane == 0 && p.lse) p.lse[head] = (M + log2f(l)) * 0.69314718055994531f;
 }
 
 // -------------------------------------------------------------------------------------- host
@@ -693,7 +747,7 @@ static cudaError_t launch(const CUtensorMap& tk, const CUtensorMap& tv, const Pa
   }
   if (e != cudaSuccess) return e;
   LaunchScope ls("paged_join", st);
-  return launch_k(paged_join_kernel<D>, dim3(p.B * p.Hk, (p.G + JT / 32 - 1) / (JT / 32)), dim3(JT), 0, st, true, p);
+  return launch_k(paged_join_kernel<D>, dim3(p.W), dim3(JT), 0, st, true, p);
 }
 
 }  // namespace pattn
@@ -742,7 +796,7 @@ hs2_status hs2_paged_attn(const hs2_bf16* Q, const void* K_pages, const void* V_
   p.wait_ns = wait_limit_ns();
   // tiles that the batch can have at most: one line of 32-bit tile numbers
   const long long span = (long long)max_pages * page_size;
-  const long long most = (long long)B * Hk * ((window > 0 && window < span ? window + tile : span) / tile + 1);
+  const long long most = (long long)B * Hk * ((window > 0 && window < span ? window + tile : span) / tile + 1 + pattn::OV);
   if (most > 0x3FFFFFFFll) return HS2_ERR_UNSUPPORTED_SHAPE;
   p.W = 2 * num_sms();
   pattn::carve(&p, workspace, B, G, d, p.W);

@@ -73,12 +73,6 @@ __device__ __forceinline__ uint32_t pack4_e4m3(const float* x) {
   asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(x[3]), "f"(x[2]));
   return (uint32_t)lo | ((uint32_t)hi << 16);
 }
-__device__ __forceinline__ void fmul2(float& dx, float& dy, float ax, float ay, float bx, float by) {
-  asm("{.reg .b64 ra, rb, rd;\n\tmov.b64 ra, {%2,%3};\n\tmov.b64 rb, {%4,%5};\n\tmul.rn.f32x2 rd, ra, rb;\n\t"
-      "mov.b64 {%0,%1}, rd;}"
-      : "=f"(dx), "=f"(dy)
-      : "f"(ax), "f"(ay), "f"(bx), "f"(by));
-}
 // d = a * b + c and d = a * b, elementwise
 __device__ __forceinline__ void fma8(V8& d, const V8& a, const V8& b, const V8& c) {
 #pragma unroll
