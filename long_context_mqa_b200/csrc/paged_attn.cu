@@ -33,7 +33,7 @@ namespace pattn {
 constexpr int NT = 192;   // TMA warp, MMA warp, four softmax warps
 constexpr int MH = 64;    // MMA rows
 constexpr int kNoPage = -2147483647 - 1;
-constexpr int MIN_TILES = 2;  // a CTA's share at least: a record costs about as much as a tile
+constexpr int MIN_TILES = 1;  // a CTA's share at least
 constexpr int OV = 2;         // what starting and ending a pair costs, in tiles
 
 struct Params {
@@ -45,11 +45,19 @@ struct Params {
   float c;       // scale log2(e), times K's scale
   float oscale;  // V's scale
   int W;         // CTAs of the grid at most in use
-  int* pre;      // [B + 1] first tile of each sequence on the line, and the tiles in all
+  int4* cuts;    // [W] of the cut before each CTA's range: pair, first CTA of the pair, its segments (0: no cut in a pair)
   float* po;     // [W][2][G][D] records
   float2* pml;   // [W][2][G]
   long long wait_ns;
   DevStatus* st;
+};
+
+constexpr int NR = 5;  // ring slots
+struct Shared {
+  uint64_t r_full[NR], r_empty[NR], q_ready, s_full, s_free, p_ready, o_full, drained;
+  uint32_t tmem_base;
+  volatile int abort_flag;
+  int warp_sum[NT / 32], start[6];
 };
 
 template <int D, bool F8>
@@ -60,9 +68,11 @@ struct Lay {
   static constexpr int SLOT = TILE * D * EB;
   static constexpr int Q_BYTES = MH * D * 2;                  // (e4m3: hi and lo terms)
   static constexpr int P_BYTES = MH * TILE * 2;
-  static constexpr int NR = F8 ? 4 : 5;
   static constexpr int OFF_P = Q_BYTES, OFF_R = OFF_P + P_BYTES;
-  static constexpr int BYTES = OFF_R + NR * SLOT + 1024;
+  // the barriers lie behind the ring and nothing is declared beside it: 1,024-byte aligned without
+  // slack, so that two CTAs with a fifth slot fit an SM
+  static constexpr int OFF_B = OFF_R + NR * SLOT;
+  static constexpr int BYTES = OFF_B + (int)sizeof(Shared);
 };
 
 __device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, long long limit, volatile int* abort_flag,
@@ -134,20 +144,24 @@ template <int TILE>
 struct Walk {
   int b, base, len, t0, n;  // the sequence, its start on the line, its length, first tile, tiles per head
   int pos, end;
+  int next_hk, at;          // the head that pos lies in, and its start on the line
   int hk, off, cnt;         // the segment: key head, first tile within the head's run, tiles
   __device__ __forceinline__ bool next(const Params& p) {
     while (pos < end) {
       const int m = pair_len(n);
       if (m > 0 && pos < base + p.Hk * m) {
-        hk = (pos - base) / m;
-        const int x = pos - base - hk * m, y = min(m, x + end - pos);
+        const int x = pos - at, y = min(m, x + end - pos);
         pos += y - x;
+        hk = next_hk;
+        if (y == m) { at += m; ++next_hk; }
         off = max(x - OV, 0);
         cnt = y - OV - off;
         if (cnt > 0) return true;
         continue;
       }
       base += p.Hk * m;
+      at = base;
+      next_hk = 0;
       ++b;
       if (b >= p.B) return false;
       n = seq_tiles<TILE>(p, b, len, t0);
@@ -179,17 +193,23 @@ template <int D, bool F8>
 __global__ void __launch_bounds__(NT, 2) paged_attn_kernel(const __grid_constant__ CUtensorMap tmK,
                                                            const __grid_constant__ CUtensorMap tmV, Params p) {
   using L = Lay<D, F8>;
-  constexpr int TILE = L::TILE, NR = L::NR, NKB = L::NKB, SLOT = L::SLOT;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+  constexpr int TILE = L::TILE, NKB = L::NKB, SLOT = L::SLOT;
+  extern __shared__ __align__(1024) uint8_t smem[];
   uint8_t *sQ = smem, *sP = smem + L::OFF_P, *sR = smem + L::OFF_R;
-  __shared__ __align__(8) uint64_t r_full[NR], r_empty[NR], q_ready, s_full, s_free, p_ready, o_full, drained;
-  __shared__ uint32_t tmem_base;
-  __shared__ volatile int abort_flag;
-  __shared__ int warp_sum[NT / 32], s_start[4];
+  Shared& sh = *reinterpret_cast<Shared*>(smem + L::OFF_B);
+  uint64_t *r_full = sh.r_full, *r_empty = sh.r_empty;
+  uint64_t &q_ready = sh.q_ready, &s_full = sh.s_full, &s_free = sh.s_free, &p_ready = sh.p_ready, &o_full = sh.o_full,
+           &drained = sh.drained;
+  uint32_t& tmem_base = sh.tmem_base;
+  volatile int& abort_flag = sh.abort_flag;
+  int *warp_sum = sh.warp_sum, *s_start = sh.start;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int nact = (p.G + 15) / 16;  // softmax warps with heads
   const long long limit = p.wait_ns;
+  if (smem_u32(smem) & 1023) {  // (the tiles' swizzle needs it; nothing is declared that could move it)
+    if (tid == 0) report_status(p.st, kStatusBounds, 700);
+    return;
+  }
 
   if (tid == 0) {
     for (int i = 0; i < NR; ++i) { mbar_init(&r_full[i], 1); mbar_init(&r_empty[i], 1); }
@@ -244,30 +264,20 @@ __global__ void __launch_bounds__(NT, 2) paged_attn_kernel(const __grid_constant
       int len, t0;
       const int n = pair_len(seq_tiles<TILE>(p, b, len, t0));
       if (r0 < at + n * p.Hk) {
-        s_start[0] = b; s_start[1] = at; s_start[2] = len; s_start[3] = t0;
+        const int hk = (r0 - at) / n;
+        s_start[0] = b; s_start[1] = at; s_start[2] = len; s_start[3] = t0; s_start[4] = hk; s_start[5] = at + hk * n;
         break;
       }
       at += n * p.Hk;
     }
   }
-  if (cta == 0) {  // for the join
-    int at = before * p.Hk;
-    for (int i = 0; i < per; ++i) {
-      const int b = tid * per + i;
-      int len, t0;
-      if (b < p.B) {
-        p.pre[b] = at;
-        at += pair_len(seq_tiles<TILE>(p, b, len, t0)) * p.Hk;
-      }
-    }
-    if (tid == 0) p.pre[p.B] = N;
-    if (bad) report_status(p.st, kStatusBounds, 701);
-  }
+  if (bad && cta == 0) report_status(p.st, kStatusBounds, 701);
   __syncthreads();
   const uint32_t tmem = tmem_base, tS = 0, tO = 128;
   Walk<TILE> wk;
   wk.pos = r0; wk.end = s_start[0] >= 0 ? r1 : r0;
   wk.b = s_start[0]; wk.base = s_start[1]; wk.len = s_start[2]; wk.t0 = s_start[3];
+  wk.next_hk = s_start[4]; wk.at = s_start[5];
   wk.n = wk.len > 0 ? (wk.len + TILE - 1) / TILE - wk.t0 : 0;
 
   if (warp == 0) {
@@ -327,7 +337,30 @@ __global__ void __launch_bounds__(NT, 2) paged_attn_kernel(const __grid_constant
     if (!ok)  // let the copies already issued land before the CTA exits
       for (uint32_t i = ri > NR ? ri - NR : 0; i < ri; ++i) mbar_wait(&r_full[i % NR], (i / NR) & 1, limit);
   } else if (warp == 1) {
-    // ------------------------------------------------------------------ MMA issuer (one thread)
+    // ------------------------------------------------------------------ MMA issuer (one thread); before
+    // the first tile can arrive the warp writes what the join has to know, and the rows of sequences without a key
+    if (lane == 1) {
+      int4 c = make_int4(0, 0, 0, 0);
+      if (s_start[0] >= 0) {
+        const int s = wk.at + OV;
+        if (r0 > s) {
+          c.x = wk.b * p.Hk + wk.next_hk;
+          c.y = split.owner(s);
+          c.z = split.owner(s + wk.n - 1) + 1 - c.y;
+        }
+      }
+      p.cuts[cta] = c;
+    }
+    for (int b = cta; b < p.B; b += gridDim.x) {
+      int len, t0;
+      if (seq_tiles<TILE>(p, b, len, t0) > 0) continue;
+      const int rows = p.Hk * p.G;
+      uint4* dst = reinterpret_cast<uint4*>(p.out + (size_t)b * rows * D);
+      for (int i = lane; i < rows * (D / 8); i += 32) dst[i] = make_uint4(0u, 0u, 0u, 0u);
+      if (p.lse)
+        for (int i = lane; i < rows; i += 32) p.lse[(size_t)b * rows + i] = -INFINITY;
+    }
+    __syncwarp();
     if (lane == 0) {
       uint32_t ri = 0, js = 0, jp = 0, nq = 0;
       bool ok = true;
@@ -623,97 +656,99 @@ __global__ void __launch_bounds__(NT, 2) paged_attn_kernel(const __grid_constant
 }
 
 // Joins the records of the (sequence, key head) pairs that several CTAs worked on, in the order of
-// their ranges, and writes the rows of sequences without a key. A pair cut into cnt segments has
-// cnt - 1 cuts inside it, and the block of each such cut joins every (cnt - 1)th of its head rows: all
-// blocks have about G records to read, however the line is cut (a block per head row left 1 MB a block
-// to read when eight long sequences share the GPU). A row's records are spread over the warps that the block
-// has to spare.
-constexpr int JT = 256, JW = JT / 32;
+// their ranges. A pair cut into cnt segments has cnt - 1 cuts inside it, and the JX blocks of each such cut join every
+// JX (cnt - 1)th of its head rows: all blocks have about G / JX records to read, however the line is cut.
+// What bounds it is the chain of dependent reads, each a microsecond's third from L2: the main kernel
+// leaves what a cut's blocks have to know in one 16-byte word, and a row's maxima, sums and accumulators are
+// asked for together. Warps that a block has to spare share a row's records.
+constexpr int JT = 256, JW = JT / 32, JX = 2;
 template <int D>
-__global__ void __launch_bounds__(JT) paged_join_kernel(Params p) {
-  constexpr int VL = D / 32;  // columns of a lane
-  __shared__ float s_acc[JW][D], s_l[JW];
-  __shared__ int s_b, s_base, s_len;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, cut = blockIdx.x + 1;
+__global__ void __launch_bounds__(JT, 4) paged_join_kernel(Params p) {
+  constexpr int VL = D / 32, U = 4;  // columns of a lane, records in flight
+  __shared__ float s_acc[JW][D];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, cut = blockIdx.x + 1;
   griddep_wait();
   griddep_launch_dependents();
-  const int N = __ldcg(p.pre + p.B);
-  const Split line(N, p.W);
-  const int at = cut < line.W ? line.start(cut) : N;
-  for (int b = tid; b < p.B; b += JT) {
-    const int x = __ldcg(p.pre + b), y = __ldcg(p.pre + b + 1);
-    if (x <= at && at < y) { s_b = b; s_base = x; s_len = y - x; }
-    if (x == y && b % gridDim.x == blockIdx.x) {
-      uint4* dst = reinterpret_cast<uint4*>(p.out + (size_t)b * p.Hk * p.G * D);
-      for (int i = 0; i < p.Hk * p.G * D / 8; ++i) dst[i] = make_uint4(0u, 0u, 0u, 0u);
-      if (p.lse)
-        for (int i = 0; i < p.Hk * p.G; ++i) p.lse[(size_t)b * p.Hk * p.G + i] = -INFINITY;
-    }
-  }
-  if (cut >= line.W) return;
-  __syncthreads();
-  const int b = s_b, base = s_base, n = s_len / p.Hk, hk = (at - base) / n;
-  const int s = base + hk * n + OV, e = s + n - OV;
-  if (at <= s) return;  // not between two tiles of a pair
-  const int w0 = line.owner(s), w1 = line.owner(e - 1) + 1;
-  const int cnt = w1 - w0, first = cut - w0 - 1;  // first < cnt - 1
-  const int rows = first < p.G ? (p.G - first + cnt - 2) / (cnt - 1) : 0;
+  const int4 c = __ldcg(p.cuts + cut);
+  const int pair = c.x, w0 = c.y, cnt = c.z;
+  if (cnt == 0) return;  // not between two tiles of a pair
+  const int step = JX * (cnt - 1), first = (cut - w0 - 1) * JX + blockIdx.y;
+  const int rows = first < p.G ? (p.G - first + step - 1) / step : 0;
   const int split = rows >= 8 ? 1 : rows >= 4 ? 2 : rows >= 2 ? 4 : 8, sub = warp % split;
   for (int k0 = 0; k0 < rows; k0 += JW / split) {
-    const int k = k0 + warp / split, row = first + k * (cnt - 1);
+    const int k = k0 + warp / split, row = first + k * step;
     const bool on = k < rows;
+    // the first segment begins its pair (record 1 of its CTA), the others begin their CTA's range
     auto rec = [&](int i) { return ((size_t)(w0 + i) * 2 + (i == 0 ? 1 : 0)) * p.G + row; };
-    float M = -INFINITY, acc[VL], l = 0.f;
+    float acc[VL], l = 0.f, M = -INFINITY;
 #pragma unroll
     for (int i = 0; i < VL; ++i) acc[i] = 0.f;
     if (on) {
-      for (int i = lane; i < cnt; i += 32) M = fmaxf(M, __ldcg(&p.pml[rec(i)]).x);
+      float o[U][VL], m[U];
+      auto load = [&](int i0) {  // records i0, i0 + split, ..
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-      const int mine = (cnt - sub + split - 1) / split;  // records sub, sub + split, ..
-      for (int i0 = 0; i0 < mine; i0 += 32) {
-        float w = 0.f;
-        if (i0 + lane < mine) {
-          const float2 ml = __ldcg(&p.pml[rec(sub + (i0 + lane) * split)]);
-          w = ml.x == -INFINITY ? 0.f : fast_exp2(ml.x - M);
-          l += ml.y * w;
-        }
-        const int m = min(32, mine - i0);
-#pragma unroll 8
-        for (int i = 0; i < m; ++i) {
-          const float wi = __shfl_sync(0xffffffffu, w, i);
-          const float* src = p.po + rec(sub + (i0 + i) * split) * D + lane * VL;
-          if constexpr (VL == 4) {
-            const float4 o = __ldcg(reinterpret_cast<const float4*>(src));
-            acc[0] += o.x * wi; acc[1] += o.y * wi; acc[2] += o.z * wi; acc[3] += o.w * wi;
-          } else {
-            const float2 o = __ldcg(reinterpret_cast<const float2*>(src));
-            acc[0] += o.x * wi; acc[1] += o.y * wi;
+        for (int u = 0; u < U; ++u) {
+          const int i = i0 + u * split;
+          m[u] = -INFINITY;
+#pragma unroll
+          for (int v = 0; v < VL; ++v) o[u][v] = 0.f;
+          if (i < cnt) {
+            const size_t r = rec(i);
+            const float* src = p.po + r * D + lane * VL;
+            if constexpr (VL == 4) {
+              const float4 x = __ldcg(reinterpret_cast<const float4*>(src));
+              o[u][0] = x.x; o[u][1] = x.y; o[u][2] = x.z; o[u][3] = x.w;
+            } else {
+              const float2 x = __ldcg(reinterpret_cast<const float2*>(src));
+              o[u][0] = x.x; o[u][1] = x.y;
+            }
+            m[u] = __ldcg(&p.pml[r].x);
           }
         }
+      };
+      float2 ml = lane < cnt ? __ldcg(&p.pml[rec(lane)]) : make_float2(-INFINITY, 0.f);
+      load(sub);
+      M = ml.x;
+      for (int i = lane + 32; i < cnt; i += 32) M = fmaxf(M, __ldcg(&p.pml[rec(i)]).x);
+#pragma unroll
+      for (int d = 16; d > 0; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
+      auto weight = [&](float x) { return x == -INFINITY ? 0.f : fast_exp2(x - M); };
+      l = ml.y * weight(ml.x);
+      for (int i = lane + 32; i < cnt; i += 32) {
+        ml = __ldcg(&p.pml[rec(i)]);
+        l += ml.y * weight(ml.x);
       }
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+      for (int d = 16; d > 0; d >>= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
+      for (int i0 = sub;;) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const float w = weight(m[u]);
+#pragma unroll
+          for (int v = 0; v < VL; ++v) acc[v] += o[u][v] * w;
+        }
+        i0 += U * split;
+        if (i0 >= cnt) break;
+        load(i0);
+      }
     }
     if (split > 1) {
       __syncthreads();
 #pragma unroll
-      for (int i = 0; i < VL; ++i) s_acc[warp][lane * VL + i] = acc[i];
-      if (lane == 0) s_l[warp] = l;
+      for (int v = 0; v < VL; ++v) s_acc[warp][lane * VL + v] = acc[v];
       __syncthreads();
       if (sub == 0)
         for (int j = 1; j < split; ++j) {
 #pragma unroll
-          for (int i = 0; i < VL; ++i) acc[i] += s_acc[warp + j][lane * VL + i];
-          l += s_l[warp + j];
+          for (int v = 0; v < VL; ++v) acc[v] += s_acc[warp + j][lane * VL + v];
         }
     }
     if (on && sub == 0) {
-      const size_t head = (size_t)(b * p.Hk + hk) * p.G + row;
+      const size_t head = (size_t)pair * p.G + row;
       const float inv = l == 0.f ? 0.f : p.oscale / l;
       uint32_t* dst = reinterpret_cast<uint32_t*>(p.out + head * D + lane * VL);
 #pragma unroll
-      for (int i = 0; i < VL; i += 2) dst[i / 2] = pack_bf16x2(acc[i] * inv, acc[i + 1] * inv);
+      for (int v = 0; v < VL; v += 2) dst[v / 2] = pack_bf16x2(acc[v] * inv, acc[v + 1] * inv);
       if (lane == 0 && p.lse) p.lse[head] = (M + log2f(l)) * 0.69314718055994531f;
     }
   }
@@ -723,11 +758,11 @@ __global__ void __launch_bounds__(JT) paged_join_kernel(Params p) {
 constexpr size_t kStatusBytes = 256;
 static size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
 
-static size_t carve(Params* p, void* ws, int B, int G, int D, int W) {
+static size_t carve(Params* p, void* ws, int G, int D, int W) {
   uint8_t* base = (uint8_t*)ws;
   size_t off = kStatusBytes;
-  if (p) { p->st = (DevStatus*)base; p->pre = (int*)(base + off); }
-  off = up256(off + (size_t)(B + 1) * 4);
+  if (p) { p->st = (DevStatus*)base; p->cuts = (int4*)(base + off); }
+  off = up256(off + (size_t)W * sizeof(int4));
   if (p) p->pml = (float2*)(base + off);
   off = up256(off + (size_t)W * 2 * G * sizeof(float2));
   if (p) p->po = (float*)(base + off);
@@ -745,9 +780,9 @@ static cudaError_t launch(const CUtensorMap& tk, const CUtensorMap& tv, const Pa
     LaunchScope ls("paged_attn", st);
     e = launch_k(paged_attn_kernel<D, F8>, dim3(p.W), dim3(NT), L::BYTES, st, true, tk, tv, p);
   }
-  if (e != cudaSuccess) return e;
+  if (e != cudaSuccess || p.W == 1) return e;
   LaunchScope ls("paged_join", st);
-  return launch_k(paged_join_kernel<D>, dim3(p.W), dim3(JT), 0, st, true, p);
+  return launch_k(paged_join_kernel<D>, dim3(p.W - 1, JX), dim3(JT), 0, st, true, p);
 }
 
 }  // namespace pattn
@@ -764,7 +799,7 @@ static bool pattn_sizes_ok(int B, int Hq, int Hk) {
 size_t hs2_paged_attn_workspace_bytes(int B, int Hq, int Hk, int d) {
   if (!pattn_sizes_ok(B, Hq, Hk) || Hq / Hk > pattn::MH || (d != 64 && d != 128)) return 0;
   const int sms = num_sms() > 0 ? num_sms() : 148;
-  return pattn::carve(nullptr, nullptr, B, Hq / Hk, d, 2 * sms);
+  return pattn::carve(nullptr, nullptr, Hq / Hk, d, 2 * sms);
 }
 
 hs2_status hs2_paged_attn(const hs2_bf16* Q, const void* K_pages, const void* V_pages, const long long* k_page_strides,
@@ -799,7 +834,7 @@ hs2_status hs2_paged_attn(const hs2_bf16* Q, const void* K_pages, const void* V_
   const long long most = (long long)B * Hk * ((window > 0 && window < span ? window + tile : span) / tile + 1 + pattn::OV);
   if (most > 0x3FFFFFFFll) return HS2_ERR_UNSUPPORTED_SHAPE;
   p.W = 2 * num_sms();
-  pattn::carve(&p, workspace, B, G, d, p.W);
+  pattn::carve(&p, workspace, G, d, p.W);
   if (most < p.W) p.W = (int)most;
   CUtensorMap tk, tv;
   if (!make_tmap_pool(&tk, K_pages, d, page_size, Hk, n_pages, k_page_strides[0], k_page_strides[1], k_page_strides[2],
