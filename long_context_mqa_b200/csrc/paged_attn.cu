@@ -519,17 +519,14 @@ __global__ void __launch_bounds__(NT, 2) paged_attn_kernel(const __grid_constant
         ++jp;
         tc_fence_after();
         const bool grown = __any_sync(0xffffffffu, al != 1.f);  // a row's maximum moved: rare after its first tiles
+        float o[OC];
 #pragma unroll
-        for (int j = 0; j < NO; ++j) {
-          float o[32];
-          tmem_ld16x2_32<OC>(tq + tO + j * 32, o);
-          tmem_ld_wait();
+        for (int j = 0; j < NO; ++j) tmem_ld16x2_32<OC>(tq + tO + j * 32, *reinterpret_cast<float(*)[32]>(o + j * 32));
+        tmem_ld_wait();
 #pragma unroll
-          for (int k = 0; k < 32; k += 2) {
-            float &x = acc[j * 32 + k], &y = acc[j * 32 + k + 1];
-            if (grown) fmul2(x, y, x, y, al, al);
-            ffma2(x, y, o[k], o[k + 1], be, be, x, y);
-          }
+        for (int k = 0; k < OC; k += 2) {
+          if (grown) fmul2(acc[k], acc[k + 1], acc[k], acc[k + 1], al, al);
+          ffma2(acc[k], acc[k + 1], o[k], o[k + 1], be, be, acc[k], acc[k + 1]);
         }
         tc_fence_before();
         return true;
@@ -555,9 +552,12 @@ __global__ void __launch_bounds__(NT, 2) paged_attn_kernel(const __grid_constant
 #pragma unroll
           for (int k = 0; k < SC; ++k) sv[k] = k >= a && k < b2 ? sv[k] : -INFINITY;
         }
-        float rm = fmaxf(sv[0], sv[1]);
+        float rx[4] = {sv[0], sv[1], sv[2], sv[3]};
 #pragma unroll
-        for (int k = 2; k < SC; k += 2) rm = fmaxf(rm, fmaxf(sv[k], sv[k + 1]));
+        for (int k = 4; k < SC; k += 8)
+#pragma unroll
+          for (int y = 0; y < 4; ++y) rx[y] = k + 4 < SC ? fmaxf(rx[y], fmaxf(sv[k + y], sv[k + 4 + y])) : fmaxf(rx[y], sv[k + y]);
+        float rm = fmaxf(fmaxf(rx[0], rx[1]), fmaxf(rx[2], rx[3]));
         rm = fmaxf(rm, __shfl_xor_sync(0xffffffffu, rm, 16));
         const float mt = rm * c;
         const float neg = mt == -INFINITY ? 0.f : F8 ? 8.f - mt : -mt;
