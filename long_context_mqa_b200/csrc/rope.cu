@@ -169,6 +169,7 @@ __global__ void __launch_bounds__(NT, 4) rope_fwd_kernel(Params p) {
   griddep_launch_dependents();
   const int t = (int)(item / p.parts), part = (int)(item % p.parts);
   if (t >= p.T) return;
+  const int pos = __ldg(p.pos + t);
   int slot = 0;
   if (PAGED) {
     slot = __ldg(p.slots + t);
@@ -190,18 +191,11 @@ __global__ void __launch_bounds__(NT, 4) rope_fwd_kernel(Params p) {
   const int per = (n_pass + p.parts - 1) / p.parts;
   const int p0 = part * per, p1 = min(n_pass, p0 + per);
   if (p0 >= p1) return;
-  if (p0 < nq + nk) angles(__ldg(p.pos + t), p.inv_freq, p.rot / 2, p.mscale, lane, sc[warp]);
+  bool fresh = false;  // the warp's angles are computed (while its first rows are on their way)
 
   // rows sub, sub + RPW, .. of passes [i0, i1) of H heads: x -> y -> put
   auto rows = [&](int i0, int i1, int H, const __nv_bfloat16* src, long long hs, const void* w, auto put) {
     V8 C, S;
-    {
-      V8 c, s, wv;
-      own.read(sc[warp], c, s);
-      own.weights(w, p.w_f32, wv);
-      mul8(C, wv, c);
-      mul8(S, Lane<D, INTER>::swap(wv), s);
-    }
     for (int i = i0; i < i1; i += U) {
       uint2 xa[U], xb[U];
 #pragma unroll
@@ -212,6 +206,15 @@ __global__ void __launch_bounds__(NT, 4) rope_fwd_kernel(Params p) {
           xa[u] = __ldg(reinterpret_cast<const uint2*>(src + h * hs + own.a));
           xb[u] = __ldg(reinterpret_cast<const uint2*>(src + h * hs + own.b));
         }
+      }
+      if (i == i0) {
+        V8 c, s, wv;
+        own.weights(w, p.w_f32, wv);
+        if (!fresh) angles(pos, p.inv_freq, p.rot / 2, p.mscale, lane, sc[warp]);
+        fresh = true;
+        own.read(sc[warp], c, s);
+        mul8(C, wv, c);
+        mul8(S, Lane<D, INTER>::swap(wv), s);
       }
 #pragma unroll
       for (int u = 0; u < U; ++u) {
@@ -290,63 +293,69 @@ __global__ void __launch_bounds__(NT, 2) rope_bwd_kernel(Params p) {
   const int per = (n_pass + p.parts - 1) / p.parts;
   const long long items = (long long)p.T * p.parts;
 
-  // passes [i0, i1) of H heads with the gradients g (bf16, or fp32) of [H, D]
+  // passes [i0, i1) of H heads with the gradients g (bf16, or fp32) of [H, D]; steps of U passes
+  // without a row missing first, as in the forward pass
+  V8 c, s;
+  int pos = 0, t = -1;
+  bool fresh = false;  // the token's angles are computed (while its first rows are on their way)
   auto rows = [&](int i0, int i1, int H, const __nv_bfloat16* src, long long hs, const void* w, const void* g, auto g32,
                   __nv_bfloat16* dst, V8& acc) {
     constexpr bool G32 = decltype(g32)::value;
-    V8 c, s, wv;
-    own.read(sc[warp], c, s);
+    constexpr int GB = G32 ? 4 : 2;
+    V8 wv;
     own.weights(w, p.w_f32, wv);
-    for (int i = i0; i < i1; i += U) {
-      uint2 xa[U], xb[U];
-      uint4 ga[U], gb[U];
+    const __nv_bfloat16 *xa = src + (i0 * RPW + sub) * hs + own.a, *xb = xa + (own.b - own.a);
+    const long long step = RPW * hs;
+    const char *ga = (const char*)g + ((i0 * RPW + sub) * D + own.a) * GB, *gb = ga + (own.b - own.a) * GB;
+    __nv_bfloat16 *da = dst + (i0 * RPW + sub) * D + own.a, *db = da + (own.b - own.a);
+    auto run = [&](int i, auto n_, auto full_) {
+      constexpr int N = decltype(n_)::value;
+      constexpr bool FULL = decltype(full_)::value;
+      const bool on = FULL || i * RPW + sub < H;
+      uint2 va[N], vb[N];
+      V8 gv[G32 ? N : 1];
+      uint2 ha[N], hb[N];
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int h = (i + u) * RPW + sub;
-        xa[u] = xb[u] = make_uint2(0u, 0u);
-        ga[u] = gb[u] = make_uint4(0u, 0u, 0u, 0u);
-        if (i + u < i1 && h < H) {
-          if (w) {
-            xa[u] = __ldg(reinterpret_cast<const uint2*>(src + h * hs + own.a));
-            xb[u] = __ldg(reinterpret_cast<const uint2*>(src + h * hs + own.b));
-          }
-          if (G32) {
-            ga[u] = __ldg(reinterpret_cast<const uint4*>((const float*)g + (long long)h * D + own.a));
-            gb[u] = __ldg(reinterpret_cast<const uint4*>((const float*)g + (long long)h * D + own.b));
-          } else {
-            const uint2 va = __ldg(reinterpret_cast<const uint2*>((const __nv_bfloat16*)g + (long long)h * D + own.a));
-            const uint2 vb = __ldg(reinterpret_cast<const uint2*>((const __nv_bfloat16*)g + (long long)h * D + own.b));
-            ga[u].x = va.x; ga[u].y = va.y;
-            gb[u].x = vb.x; gb[u].y = vb.y;
-          }
+      for (int u = 0; u < N; ++u) {
+        va[u] = vb[u] = ha[u] = hb[u] = make_uint2(0u, 0u);
+        if (w && on) {
+          va[u] = __ldg(reinterpret_cast<const uint2*>(xa));
+          vb[u] = __ldg(reinterpret_cast<const uint2*>(xb));
+        }
+        xa += step;
+        xb += step;
+        if constexpr (G32) {
+          const float4 z = make_float4(0.f, 0.f, 0.f, 0.f);
+          const float4 q0 = on ? __ldg(reinterpret_cast<const float4*>(ga + u * (RPW * D * GB))) : z;
+          const float4 q1 = on ? __ldg(reinterpret_cast<const float4*>(gb + u * (RPW * D * GB))) : z;
+          gv[u].x[0] = q0.x; gv[u].x[1] = q0.y; gv[u].x[2] = q0.z; gv[u].x[3] = q0.w;
+          gv[u].x[4] = q1.x; gv[u].x[5] = q1.y; gv[u].x[6] = q1.z; gv[u].x[7] = q1.w;
+        } else if (on) {
+          ha[u] = __ldg(reinterpret_cast<const uint2*>(ga + u * (RPW * D * GB)));
+          hb[u] = __ldg(reinterpret_cast<const uint2*>(gb + u * (RPW * D * GB)));
         }
       }
+      if (!fresh) {
+        angles(pos, p.inv_freq, p.rot / 2, p.mscale, lane, sc[warp]);
+        own.read(sc[warp], c, s);
+        s = Lane<D, INTER>::swap(s);  // the transpose: n = y c + partner s, with the partner's s
+        fresh = true;
+      }
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        if (i + u >= i1) break;  // (warp-uniform)
-        const int h = (i + u) * RPW + sub;
-        V8 x, y, n;
-        unpack4(xa[u], x.x);
-        unpack4(xb[u], x.x + 4);
-        if (G32) {
-          const uint32_t v[8] = {ga[u].x, ga[u].y, ga[u].z, ga[u].w, gb[u].x, gb[u].y, gb[u].z, gb[u].w};
-#pragma unroll
-          for (int e = 0; e < 8; ++e) y.x[e] = __uint_as_float(v[e]);
+      for (int u = 0; u < N; ++u) {
+        V8 y, n;
+        if constexpr (G32) {
+          y = gv[u];
         } else {
-          unpack4(make_uint2(ga[u].x, ga[u].y), y.x);
-          unpack4(make_uint2(gb[u].x, gb[u].y), y.x + 4);
+          unpack4(ha[u], y.x);
+          unpack4(hb[u], y.x + 4);
         }
-        // the transpose: n = y c - partner s, with each element's own s
         mul8(n, y, c);
-        if (own.on) {
-          V8 ys;
-          mul8(ys, y, s);  // partner's s is this element's, negated: n_a gets + y_b s_b
-          const V8 t2 = Lane<D, INTER>::swap(ys);
-#pragma unroll
-          for (int e = 0; e < 8; e += 2) fadd2(n.x[e], n.x[e + 1], n.x[e], n.x[e + 1], t2.x[e], t2.x[e + 1]);
-        }
+        if (own.on) fma8(n, Lane<D, INTER>::swap(y), s, n);
         if (w) {
-          V8 u8, gx;
+          V8 x, u8, gx;
+          unpack4(va[u], x.x);
+          unpack4(vb[u], x.x + 4);
           mul8(u8, n, wv);
           mul8(gx, n, x);
           const float r = rsqrtf(row_sum<LPR>(dot8(x, x)) * (1.f / D) + p.eps);
@@ -358,18 +367,26 @@ __global__ void __launch_bounds__(NT, 2) rope_bwd_kernel(Params p) {
             ffma2(n.x[e], n.x[e + 1], x.x[e], x.x[e + 1], -m, -m, u8.x[e], u8.x[e + 1]);
           }
         }
-        if (h < H) {
-          *reinterpret_cast<uint2*>(dst + (long long)h * D + own.a) = pack4(n.x);
-          *reinterpret_cast<uint2*>(dst + (long long)h * D + own.b) = pack4(n.x + 4);
+        if (on) {
+          *reinterpret_cast<uint2*>(da + u * (RPW * D)) = pack4(n.x);
+          *reinterpret_cast<uint2*>(db + u * (RPW * D)) = pack4(n.x + 4);
         }
       }
-    }
+      ga += N * (RPW * D * GB); gb += N * (RPW * D * GB);
+      da += N * (RPW * D); db += N * (RPW * D);
+    };
+    const int full = min(i1, H / RPW);
+    int i = i0;
+    for (; i + U <= full; i += U) run(i, std::integral_constant<int, U>{}, std::true_type{});
+    for (; i < i1; ++i) run(i, std::integral_constant<int, 1>{}, std::false_type{});
   };
   for (long long item = (long long)blockIdx.x * NW + warp; item < items; item += (long long)gridDim.x * NW) {
-    const int t = (int)(item / p.parts), part = (int)(item % p.parts);
+    const int part = (int)(item % p.parts);
+    t = (int)(item / p.parts);
     const int p0 = part * per, p1 = min(n_pass, p0 + per);
     if (p0 >= p1) continue;
-    angles(__ldg(p.pos + t), p.inv_freq, p.rot / 2, p.mscale, lane, sc[warp]);
+    pos = __ldg(p.pos + t);
+    fresh = false;
     if (p0 < nq)
       rows(p0, min(p1, nq), p.Hq, p.q + t * p.q_ts, p.q_hs, p.qw, p.dq_out + (long long)t * p.Hq * D, std::false_type{},
            p.dq + (long long)t * p.Hq * D, aq);
