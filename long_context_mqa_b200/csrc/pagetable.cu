@@ -9,10 +9,9 @@
 //
 // The work is a prefix sum over at most 4,096 requests and then independent items: one per token row
 // and one per returned page, each finding its request by a binary search in the sums. Every block
-// computes the sums for itself (16 KB of lengths from L2, three block scans), which costs less than a
+// computes the sums for itself (16 KB of lengths from L2, three scans in step), which costs less than a
 // second launch or a grid-wide wait, and takes its share of the items. The token that is the first of
-// its page writes the table entry. The last block to have read the inputs writes the new lengths and
-// the ring's state, so that both may be updated in place.
+// its page writes the table entry. Latency bounds it: two reads that depend on one another, the scan between them.
 #include "host_util.h"
 #include "tc.cuh"
 
@@ -21,7 +20,6 @@ namespace ptab {
 
 constexpr int NT = 512;
 constexpr int MAX_B = 4096;
-constexpr int PER = MAX_B / NT;  // requests of a thread at most
 
 struct Params {
   int32_t* table;
@@ -39,30 +37,6 @@ struct Params {
 constexpr int MOST = (1 << 30) - 1;
 __device__ __forceinline__ int sat_add(int a, int b) { return min(a + b, MOST); }
 
-// exclusive prefix sum of one value per thread (0 .. MOST) over the block, and its total
-__device__ __forceinline__ int block_scan(int v, int* total, int* warp_sum) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int x = v;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int y = __shfl_up_sync(0xffffffffu, x, o);
-    if (lane >= o) x = sat_add(x, y);
-  }
-  __syncthreads();
-  if (lane == 31) warp_sum[warp] = x;
-  __syncthreads();
-  int before = 0, all = 0;
-#pragma unroll
-  for (int w = 0; w < NT / 32; ++w) {
-    const int s = warp_sum[w];
-    if (w < warp) before = sat_add(before, s);
-    all = sat_add(all, s);
-  }
-  *total = all;
-  const int prev = __shfl_up_sync(0xffffffffu, x, 1);
-  return lane == 0 ? before : sat_add(before, prev);
-}
-
 // the request whose range [off[b], off[b + 1]) holds i (ranges may be empty)
 __device__ __forceinline__ int find(const int* off, int n, int i) {
   int lo = 0, hi = n;  // off[lo] <= i < off[hi]
@@ -74,75 +48,111 @@ __device__ __forceinline__ int find(const int* off, int n, int i) {
   return lo;
 }
 
+// PER: requests of a thread
+template <int PER>
 __global__ void __launch_bounds__(NT) page_table_kernel(Params p) {
   extern __shared__ int sm[];
   int* tok = sm;               // [B + 1] first packed row of each request
   int* add = tok + p.B + 1;    // [B] its first new page, counted from the ring's head; -1: not granted
   int* back = add + p.B;       // [B + 1] its first returned page
-  __shared__ int warp_sum[NT / 32];
-  __shared__ int s_used, s_last;
+  int* held_len = back + p.B + 1;  // [B] its length; of one that gives pages back, how many it keeps
+  __shared__ int warp_sum[3][NT / 32], s_used, s_last;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (tid == 0) s_used = 0;
   griddep_wait();
   griddep_launch_dependents();
-  const int tid = threadIdx.x;
   const int head = p.state[0], count = p.state[1];
-  const bool state_ok = head >= 0 && head < p.cap && count >= 0 && count <= p.cap;
-  const int per = (p.B + NT - 1) / NT;
-  if (tid == 0) s_used = 0;
   // what each request adds: token rows, pages it lacks, pages it gives back
-  int len[PER], rows[PER], grow[PER], gone[PER], want_len[PER];
-  int sr = 0, sg = 0, sb = 0;
+  int len[PER], rows[PER], grow[PER], gone[PER], want_len[PER], sum[3] = {0, 0, 0};
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    const int b = tid * PER + i;
+    len[i] = b < p.B ? p.lens[b] : 0;
+    rows[i] = b < p.B ? p.delta[b] : 0;
+  }
+  const bool state_ok = head >= 0 && head < p.cap && count >= 0 && count <= p.cap;
   bool bad = !state_ok;
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
-    len[i] = rows[i] = grow[i] = gone[i] = want_len[i] = 0;
-    const int b = tid * per + i;
-    if (i < per && b < p.B) {
-      const int n = p.lens[b], x = p.delta[b];
-      const long long m = (long long)n + x;
-      len[i] = n;
-      rows[i] = x > 0 ? min(x, MOST) : 0;
-      // a length or an end outside the table: the request is left as it is
-      if (n < 0 || m < 0 || n > (long long)p.width * p.page || m > (long long)p.width * p.page) {
-        bad = true;
-        want_len[i] = n;
-        grow[i] = -1;
-      } else {
-        want_len[i] = (int)m;
-        const int held = (n + p.page - 1) / p.page, want = (int)((m + p.page - 1) / p.page);
-        grow[i] = want > held ? want - held : 0;
-        gone[i] = held > want ? held - want : 0;
-      }
-      sr = sat_add(sr, rows[i]);
-      sg = sat_add(sg, max(grow[i], 0));
-      sb = sat_add(sb, gone[i]);
+    const int n = len[i], x = rows[i], b = tid * PER + i;
+    const long long m = (long long)n + x;
+    int keep = n;
+    grow[i] = gone[i] = 0;
+    rows[i] = x > 0 ? min(x, MOST) : 0;
+    // a length or an end outside the table: the request is left as it is
+    if (n < 0 || m < 0 || n > (long long)p.width * p.page || m > (long long)p.width * p.page) {
+      bad = true;
+      want_len[i] = n;
+      grow[i] = -1;
+    } else {
+      want_len[i] = (int)m;
+      const int held = (n + p.page - 1) / p.page, want = (int)((m + p.page - 1) / p.page);
+      grow[i] = want > held ? want - held : 0;
+      gone[i] = held > want ? held - want : 0;
+      if (gone[i] > 0) keep = want;
     }
+    if (b < p.B) held_len[b] = keep;
+    sum[0] = sat_add(sum[0], rows[i]);
+    sum[1] = sat_add(sum[1], max(grow[i], 0));
+    sum[2] = sat_add(sum[2], gone[i]);
   }
-  int rows_all, grow_all, back_all;
-  int r0 = block_scan(sr, &rows_all, warp_sum);
-  int g0 = block_scan(sg, &grow_all, warp_sum);
-  int b0 = block_scan(sb, &back_all, warp_sum);
+  // the three exclusive prefix sums over the block (saturating: every value is >= 0), and their totals
+  int at[3], all[3];
+#pragma unroll
+  for (int k = 0; k < 3; ++k) {
+    int x = sum[k];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x = sat_add(x, y);
+    }
+    if (lane == 31) warp_sum[k][warp] = x;
+    const int prev = __shfl_up_sync(0xffffffffu, x, 1);
+    at[k] = lane == 0 ? 0 : prev;
+  }
+  __syncthreads();
+  // the inputs have been read; the block that is the last to say so writes the new lengths and the
+  // ring's state at its end, so that they may be updated in place
+  if (gridDim.x > 1 && tid == NT - 1) {
+    __threadfence();
+    s_last = atomicAdd(p.done, 1u) == gridDim.x - 1;
+  }
+#pragma unroll
+  for (int k = 0; k < 3; ++k) {
+    int x = lane < NT / 32 ? warp_sum[k][lane] : 0;
+#pragma unroll
+    for (int o = 1; o < NT / 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x = sat_add(x, y);
+    }
+    all[k] = __shfl_sync(0xffffffffu, x, NT / 32 - 1);
+    const int before = __shfl_sync(0xffffffffu, x, warp > 0 ? warp - 1 : 0);
+    if (warp > 0) at[k] = sat_add(before, at[k]);
+  }
+  const int rows_all = all[0], back_all = all[2];
   const int avail = state_ok ? count : 0;
   int used = 0;
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
-    const int b = tid * per + i;
-    if (i < per && b < p.B) {
-      tok[b] = r0;
-      back[b] = b0;
-      r0 = sat_add(r0, rows[i]);
-      b0 = sat_add(b0, gone[i]);
-      bool granted = grow[i] >= 0;
-      if (grow[i] > 0) {
-        granted = g0 <= avail && grow[i] <= avail - g0;  // in request order, while they last
-        if (granted) used = g0 + grow[i];
-        else bad = true;
-      }
-      add[b] = granted ? g0 : -1;
-      g0 = sat_add(g0, max(grow[i], 0));
-      if (!granted) want_len[i] = len[i];
+    const int b = tid * PER + i;
+    bool granted = grow[i] >= 0;
+    if (grow[i] > 0) {
+      granted = at[1] <= avail && grow[i] <= avail - at[1];  // in request order, while they last
+      if (granted) used = at[1] + grow[i];
+      else bad = true;
     }
+    if (b < p.B) {
+      tok[b] = at[0];
+      back[b] = at[2];
+      add[b] = granted ? at[1] : -1;
+    }
+    at[0] = sat_add(at[0], rows[i]);
+    at[1] = sat_add(at[1], max(grow[i], 0));
+    at[2] = sat_add(at[2], gone[i]);
+    if (!granted) want_len[i] = len[i];
   }
-  if (used > 0) atomicMax(&s_used, used);
+  used = __reduce_max_sync(0xffffffffu, used);
+  if (lane == 0 && used > 0) atomicMax(&s_used, used);
   if (tid == 0) {
     tok[p.B] = rows_all;
     back[p.B] = back_all;
@@ -154,58 +164,51 @@ __global__ void __launch_bounds__(NT) page_table_kernel(Params p) {
   const bool any_bad = __syncthreads_or(bad);
   if (any_bad && blockIdx.x == 0 && tid == 0) report_status(p.st, kStatusBounds, 601);
 
-  const long long items = (long long)p.T + (room ? back_all : 0);
-  const long long step = (long long)gridDim.x * NT;
-  for (long long it = (long long)blockIdx.x * NT + tid; it < items; it += step) {
+  auto wrap = [&](unsigned i) { return i >= (unsigned)p.cap ? i - (unsigned)p.cap : i; };  // i < 2 cap
+  const unsigned items = (unsigned)p.T + (unsigned)(room ? back_all : 0);  // (both below 2^30)
+  for (unsigned i0 = blockIdx.x * NT + tid; i0 < items; i0 += gridDim.x * NT) {
+    const int it = (int)i0;
     if (it < p.T) {
-      const int row = (int)it;
       int pos = -1;
       long long slot = -1;
-      if (row < rows_all) {
-        const int b = find(tok, p.B, row);
-        const int n = p.lens[b], first = add[b];
-        pos = n + row - tok[b];
+      if (it < rows_all) {
+        const int b = find(tok, p.B, it), n = held_len[b], first = add[b];
+        pos = n + it - tok[b];
         if (first >= 0) {
           const int j = pos / p.page, r = pos - j * p.page, held = (n + p.page - 1) / p.page;
           int pg;
           if (j < held) {
             pg = p.table[(size_t)b * p.width + j];
           } else {
-            pg = p.ring[((long long)head + first + j - held) % p.cap];
+            pg = p.ring[wrap((unsigned)head + (unsigned)(first + j - held))];
             if (r == 0) p.table[(size_t)b * p.width + j] = pg;
           }
           slot = (long long)pg * p.page + r;
           if (pg < 0 || slot > 0x7FFFFFFFll) slot = -1;
         }
       }
-      p.pos[row] = pos;
-      p.slots[row] = (int)slot;
+      p.pos[it] = pos;
+      p.slots[it] = (int)slot;
     } else {
-      const int i = (int)(it - p.T);
-      const int b = find(back, p.B, i);
-      const int want = (p.lens[b] + p.delta[b] + p.page - 1) / p.page;
-      p.ring[((long long)head + count + i) % p.cap] = p.table[(size_t)b * p.width + want + i - back[b]];
+      const int i = it - p.T, b = find(back, p.B, i);
+      p.ring[wrap((unsigned)head + (unsigned)(count + i))] = p.table[(size_t)b * p.width + held_len[b] + i - back[b]];
     }
   }
   if (blockIdx.x == 0)
     for (int b = tid; b <= p.B; b += NT) p.cu[b] = tok[b];
-  // the last block to get here has seen every other one read the inputs
-  __syncthreads();
-  if (tid == 0) {
-    __threadfence();
-    s_last = atomicAdd(p.done, 1u) == gridDim.x - 1;
+  if (gridDim.x > 1) {
+    __syncthreads();
+    if (!s_last) return;
   }
-  __syncthreads();
-  if (!s_last) return;
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
-    const int b = tid * per + i;
-    if (i < per && b < p.B) p.lens_out[b] = want_len[i];
+    const int b = tid * PER + i;
+    if (b < p.B) p.lens_out[b] = want_len[i];
   }
   if (tid == 0) {
-    *p.done = 0;
+    if (gridDim.x > 1) *p.done = 0;
     const int u = s_used;
-    p.state_out[0] = state_ok ? (int)(((long long)head + u) % p.cap) : head;
+    p.state_out[0] = state_ok ? (int)wrap((unsigned)head + (unsigned)u) : head;
     p.state_out[1] = state_ok ? count - u + (room ? back_all : 0) : count;
   }
 }
@@ -236,18 +239,24 @@ hs2_status hs2_page_table_update(int32_t* page_table, int B, int max_pages, cons
   ptab::Params p{page_table, lens, delta, free_ring, free_state, lens_out, free_state_out, cu_tokens, positions, slots,
                  B, max_pages, ring_size, page_size, max_tokens,
                  (unsigned*)((uint8_t*)workspace + ptab::kDoneOffset), (DevStatus*)workspace};
-  // one block per 2,048 rows: a decode step is one block's work, a prompt's rows spread over the GPU
-  int grid = (max_tokens + 2047) / 2048;
-  if (grid < 1) grid = 1;
-  if (grid > num_sms()) grid = num_sms();
-  const size_t smem = (size_t)(3 * B + 2) * sizeof(int);
-  if (smem > 48000 && cudaFuncSetAttribute(ptab::page_table_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                           (int)((3 * ptab::MAX_B + 2) * sizeof(int))) != cudaSuccess)
-    return HS2_ERR_CUDA;
-  LaunchScope ls("page_table", (cudaStream_t)stream);
-  return launch_k(ptab::page_table_kernel, dim3(grid), dim3(ptab::NT), smem, (cudaStream_t)stream, true, p) == cudaSuccess
-             ? HS2_OK
-             : HS2_ERR_CUDA;
+  // a row a thread, while there are threads: a decode step is one block's work (a row waits for a page id from
+  // L2 or HBM, so rows in turn cost that each: 511 requests with 105,000 rows 9.9 us at four rows a thread)
+  const long long blocks = ((long long)max_tokens + ptab::NT - 1) / ptab::NT, most = 2ll * num_sms();
+  const int grid = (int)(blocks < 1 ? 1 : blocks > most ? most : blocks);
+  const size_t smem = (size_t)(4 * B + 2) * sizeof(int);
+  const cudaStream_t st = (cudaStream_t)stream;
+  cudaError_t e;
+  if (B <= ptab::NT) {
+    LaunchScope ls("page_table", st);
+    e = launch_k(ptab::page_table_kernel<1>, dim3(grid), dim3(ptab::NT), smem, st, true, p);
+  } else {
+    e = cudaFuncSetAttribute(ptab::page_table_kernel<ptab::MAX_B / ptab::NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             (int)((4 * ptab::MAX_B + 2) * sizeof(int)));
+    if (e != cudaSuccess) return HS2_ERR_CUDA;
+    LaunchScope ls("page_table", st);
+    e = launch_k(ptab::page_table_kernel<ptab::MAX_B / ptab::NT>, dim3(grid), dim3(ptab::NT), smem, st, true, p);
+  }
+  return e == cudaSuccess ? HS2_OK : HS2_ERR_CUDA;
 }
 
 }  // extern "C"
