@@ -52,9 +52,9 @@ struct Params {
   DevStatus* st;
 };
 
-constexpr int NR = 5;  // ring slots
+constexpr int MAX_NR = 5;
 struct Shared {
-  uint64_t r_full[NR], r_empty[NR], q_ready, s_full, s_free, p_ready, o_full, drained;
+  uint64_t r_full[MAX_NR], r_empty[MAX_NR], q_ready, s_full, s_free, p_ready, o_full, drained;
   uint32_t tmem_base;
   volatile int abort_flag;
   int warp_sum[NT / 32], start[6];
@@ -68,7 +68,8 @@ struct Lay {
   static constexpr int SLOT = TILE * D * EB;
   static constexpr int Q_BYTES = MH * D * 2;                  // (e4m3: hi and lo terms)
   static constexpr int P_BYTES = MH * TILE * 2;
-  static constexpr int OFF_P = Q_BYTES, OFF_R = OFF_P + P_BYTES;
+  static constexpr int NR = F8 || D == 64 ? 4 : 5;            // ring slots
+  static constexpr int OFF_P = Q_BYTES, OFF_R = OFF_P + 2 * P_BYTES;  // (P of two tiles)
   // the barriers lie behind the ring and nothing is declared beside it: 1,024-byte aligned without
   // slack, so that two CTAs with a fifth slot fit an SM
   static constexpr int OFF_B = OFF_R + NR * SLOT;
@@ -193,7 +194,7 @@ template <int D, bool F8>
 __global__ void __launch_bounds__(NT, 2) paged_attn_kernel(const __grid_constant__ CUtensorMap tmK,
                                                            const __grid_constant__ CUtensorMap tmV, Params p) {
   using L = Lay<D, F8>;
-  constexpr int TILE = L::TILE, NKB = L::NKB, SLOT = L::SLOT;
+  constexpr int TILE = L::TILE, NR = L::NR, NKB = L::NKB, SLOT = L::SLOT;
   extern __shared__ __align__(1024) uint8_t smem[];
   uint8_t *sQ = smem, *sP = smem + L::OFF_P, *sR = smem + L::OFF_R;
   Shared& sh = *reinterpret_cast<Shared*>(smem + L::OFF_B);
@@ -397,6 +398,7 @@ __global__ void __launch_bounds__(NT, 2) paged_attn_kernel(const __grid_constant
         // P is in shared memory (and the accumulator of the tile before it has been read)
         if (!wait_bar(&p_ready, jp & 1, limit, &abort_flag, p.st, 714)) return false;
         tc_fence_after();
+        const uint32_t pb = (jp & 1) * L::P_BYTES;
         if constexpr (F8) {
           constexpr uint32_t ID = idesc_e4m3(MH, D, 0, 1);
           const uint64_t va = sdesc(smem_u32(sR + s * SLOT), TILE * 128, 1024);
@@ -404,13 +406,13 @@ __global__ void __launch_bounds__(NT, 2) paged_attn_kernel(const __grid_constant
           for (int h = 0; h < 2; ++h)  // P's hi and lo terms
 #pragma unroll
             for (int kk = 0; kk < TILE / 32; ++kk)
-              umma_f8(tmem + tO, sdesc_at(pa, h * (MH * 128) + kk * 32), sdesc_at(va, kk * 4096), ID, h + kk > 0);
+              umma_f8(tmem + tO, sdesc_at(pa, pb + h * (MH * 128) + kk * 32), sdesc_at(va, kk * 4096), ID, h + kk > 0);
         } else {
           constexpr uint32_t ID = idesc_bf16(MH, D, 0, 1);
           const uint64_t va = sdesc(smem_u32(sR + s * SLOT), TILE * 128, 1024);
 #pragma unroll
           for (int kk = 0; kk < TILE / 16; ++kk)
-            umma_ss(tmem + tO, sdesc_at(pa, (kk / 4) * (MH * 128) + (kk % 4) * 32), sdesc_at(va, kk * 2048), ID, kk > 0);
+            umma_ss(tmem + tO, sdesc_at(pa, pb + (kk / 4) * (MH * 128) + (kk % 4) * 32), sdesc_at(va, kk * 2048), ID, kk > 0);
         }
         umma_commit(&o_full);
         umma_commit(&r_empty[s]);
@@ -562,28 +564,39 @@ __global__ void __launch_bounds__(NT, 2) paged_attn_kernel(const __grid_constant
         const float mt = rm * c;
         const float neg = mt == -INFINITY ? 0.f : F8 ? 8.f - mt : -mt;
         float la = 0.f, lb = 0.f;
-        uint32_t pk[SC / 2];  // bf16 pairs; e4m3: the hi codes of four keys, then the lo codes
+        // P -> shared memory, K-major, 16 bytes of codes as soon as they are there
+        const uint32_t pb = smem_u32(sP) + ((js - 1) & 1) * L::P_BYTES;
+        constexpr int CK = F8 ? 16 : 8;  // keys of a chunk
 #pragma unroll
-        for (int k = 0; k < SC; k += 4) {
-          float e[4];
-          ffma2(e[0], e[1], sv[k], sv[k + 1], c, c, neg, neg);
-          ffma2(e[2], e[3], sv[k + 2], sv[k + 3], c, c, neg, neg);
+        for (int k0 = 0; k0 < SC; k0 += CK) {
+          uint32_t pk[CK / 2];  // bf16 pairs; e4m3: the hi codes of four keys, then the lo codes
 #pragma unroll
-          for (int y = 0; y < 4; ++y) e[y] = fast_exp2(e[y]);
-          fadd2(la, lb, la, lb, e[0], e[1]);
-          fadd2(la, lb, la, lb, e[2], e[3]);
-          if constexpr (F8) {
-            uint32_t h0, l0, h1, l1;
-            split_e4m3(pack_f16x2(e[0], e[1]), h0, l0);
-            split_e4m3(pack_f16x2(e[2], e[3]), h1, l1);
-            pk[k / 4] = h0 | (h1 << 16);
-            pk[SC / 4 + k / 4] = l0 | (l1 << 16);
-          } else {
-            pk[k / 2] = pack_bf16x2(e[0], e[1]);
-            pk[k / 2 + 1] = pack_bf16x2(e[2], e[3]);
+          for (int k = 0; k < CK; k += 4) {
+            float e[4];
+            const float* v = sv + k0 + k;
+            ffma2(e[0], e[1], v[0], v[1], c, c, neg, neg);
+            ffma2(e[2], e[3], v[2], v[3], c, c, neg, neg);
+#pragma unroll
+            for (int y = 0; y < 4; ++y) e[y] = fast_exp2(e[y]);
+            fadd2(la, lb, la, lb, e[0], e[1]);
+            fadd2(la, lb, la, lb, e[2], e[3]);
+            if constexpr (F8) {
+              uint32_t h0, l0, h1, l1;
+              split_e4m3(pack_f16x2(e[0], e[1]), h0, l0);
+              split_e4m3(pack_f16x2(e[2], e[3]), h1, l1);
+              pk[k / 4] = h0 | (h1 << 16);
+              pk[CK / 4 + k / 4] = l0 | (l1 << 16);
+            } else {
+              pk[k / 2] = pack_bf16x2(e[0], e[1]);
+              pk[k / 2 + 1] = pack_bf16x2(e[2], e[3]);
+            }
           }
+          const int ch = (s0 + k0) / CK;
+          const uint32_t dst = pb + (ch / 8) * (MH * 128) + sw128_off(row, ch % 8);
+          st_shared_v4(dst, pk[0], pk[1], pk[2], pk[3]);
+          if constexpr (F8) st_shared_v4(dst + MH * 128, pk[4], pk[5], pk[6], pk[7]);
         }
-        // the last tile's product before P is overwritten
+        // the last tile's product before this tile's may overwrite it
         if (i > 0 && !add_o()) { ok = false; break; }
         // factors of this tile's product
         const float mn = fmaxf(m_run, mt);
@@ -591,23 +604,6 @@ __global__ void __launch_bounds__(NT, 2) paged_attn_kernel(const __grid_constant
         be = mt == -INFINITY ? 0.f : (F8 ? 0.00390625f : 1.f) * fast_exp2(mt - mn);
         l_run = l_run * al + (la + lb) * be;
         m_run = mn;
-        // ---- P -> shared memory, K-major
-        if constexpr (F8) {
-#pragma unroll
-          for (int y = 0; y < SC / 16; ++y) {
-            const uint32_t dst = smem_u32(sP) + sw128_off(row, s0 / 16 + y);
-            st_shared_v4(dst, pk[4 * y], pk[4 * y + 1], pk[4 * y + 2], pk[4 * y + 3]);
-            st_shared_v4(dst + MH * 128, pk[SC / 4 + 4 * y], pk[SC / 4 + 4 * y + 1], pk[SC / 4 + 4 * y + 2],
-                         pk[SC / 4 + 4 * y + 3]);
-          }
-        } else {
-#pragma unroll
-          for (int y = 0; y < SC / 8; ++y) {
-            const int ch = s0 / 8 + y;
-            st_shared_v4(smem_u32(sP) + (ch / 8) * (MH * 128) + sw128_off(row, ch % 8), pk[4 * y], pk[4 * y + 1],
-                         pk[4 * y + 2], pk[4 * y + 3]);
-          }
-        }
         if (lo > 0 || hi < TILE) {
           // rows of V that no key is in may hold anything, and 0 times an infinity or a NaN is not 0
           const uint32_t vi = ring + (i == cnt - 1 ? 2 * cnt - 1 : 2 * i + 2);
