@@ -702,16 +702,19 @@ __global__ void __launch_bounds__(JT, 4) paged_join_kernel(Params p) {
           }
         }
       };
-      float2 ml = lane < cnt ? __ldcg(&p.pml[rec(lane)]) : make_float2(-INFINITY, 0.f);
+      // maxima and sums of the first 64 records, a lane two; there are rarely more
+      const float2 none = make_float2(-INFINITY, 0.f);
+      const float2 m0 = lane < cnt ? __ldcg(&p.pml[rec(lane)]) : none;
+      const float2 m1 = lane + 32 < cnt ? __ldcg(&p.pml[rec(lane + 32)]) : none;
       load(sub);
-      M = ml.x;
-      for (int i = lane + 32; i < cnt; i += 32) M = fmaxf(M, __ldcg(&p.pml[rec(i)]).x);
+      M = fmaxf(m0.x, m1.x);
+      for (int i = lane + 64; i < cnt; i += 32) M = fmaxf(M, __ldcg(&p.pml[rec(i)]).x);
 #pragma unroll
       for (int d = 16; d > 0; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
       auto weight = [&](float x) { return x == -INFINITY ? 0.f : fast_exp2(x - M); };
-      l = ml.y * weight(ml.x);
-      for (int i = lane + 32; i < cnt; i += 32) {
-        ml = __ldcg(&p.pml[rec(i)]);
+      l = m0.y * weight(m0.x) + m1.y * weight(m1.x);
+      for (int i = lane + 64; i < cnt; i += 32) {
+        const float2 ml = __ldcg(&p.pml[rec(i)]);
         l += ml.y * weight(ml.x);
       }
 #pragma unroll

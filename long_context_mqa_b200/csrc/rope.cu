@@ -427,8 +427,14 @@ __global__ void __launch_bounds__(1024) rope_dw_kernel(const float* part, int n,
   griddep_launch_dependents();
   const int c = blockIdx.x * 32 + (threadIdx.x & 31), strip = threadIdx.x >> 5;
   float a = 0.f;
-#pragma unroll 4
-  for (int i = strip; i < n; i += 32) a += __ldcg(part + (size_t)i * 2 * D + c);
+  constexpr int U = 10;  // records in flight: two rounds of reads for the 592 there are at most on 148 SMs
+  for (int i = strip; i < n; i += 32 * U) {
+    float v[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) v[u] = i + 32 * u < n ? __ldcg(part + (size_t)(i + 32 * u) * 2 * D + c) : 0.f;
+#pragma unroll
+    for (int u = 0; u < U; ++u) a += v[u];
+  }
   s[strip][threadIdx.x & 31] = a;
   __syncthreads();
   if (strip == 0) {
