@@ -469,12 +469,15 @@ HS2_API hs2_status hs2_paged_attn(const hs2_bf16* Q, const void* K_pages, const 
  * returns HS2_OK, HS2_ERR_DEVICE_TIMEOUT or HS2_ERR_DEVICE_BOUNDS (HS2_ERR_CUDA if the
  * read failed). hs2_clear_device_status: zeroes the status block (the word and the grid
  * barrier's counters; asynchronously, on `stream`).
+ * hs2_stream_capturing: nonzero while `stream` is being captured into a graph (a caller that keeps
+ * workspaces gives a captured call one that lives as long as the graph).
  * hs2_set_wait_limit_ns: wall-time bound of every device-side wait of later launches
  * (default 2 s, or the environment variable HS2_WAIT_LIMIT_MS at first use).
  * hs2_selftest_wait_timeout: launches one kernel whose bounded wait is on a barrier that
  * nothing completes; it gives up after `limit_ns`, records HS2_ERR_DEVICE_TIMEOUT in the
  * status word and returns, leaving the context usable (a failure-detection test hook).
  */
+HS2_API int hs2_stream_capturing(hs2_stream stream);
 HS2_API hs2_status hs2_read_device_status(const void* workspace, hs2_stream stream);
 HS2_API hs2_status hs2_clear_device_status(void* workspace, hs2_stream stream);
 HS2_API void hs2_set_wait_limit_ns(long long limit_ns);

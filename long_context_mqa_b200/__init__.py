@@ -21,6 +21,7 @@ h [T, hidden] bf16, w [n_layers, 2, hidden, d] bf16 -> kv [n_layers, 2, T, d] bf
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 import os
 import threading
@@ -125,6 +126,8 @@ def _load_library() -> ctypes.CDLL:
     lib.hs2_paged_attn.argtypes = [P, P, P, P, P, i32, i32, P, i32, P, i32, i32, i32, i32, i32, f32, f32, f32, i32, P, P,
                                    P, sz, P]
     lib.hs2_paged_attn.restype = i32
+    lib.hs2_stream_capturing.argtypes = [P]
+    lib.hs2_stream_capturing.restype = i32
     lib.hs2_read_device_status.argtypes = [P, P]
     lib.hs2_read_device_status.restype = i32
     lib.hs2_clear_device_status.argtypes = [P, P]
@@ -163,7 +166,8 @@ def _load_marshalling():
     addr = lambda f: ctypes.cast(f, ctypes.c_void_p).value
     mod.set_entries(addr(lib.hs2_full_attn_select), addr(lib.hs2_sparse_attn))
     mod.set_cache_entries(addr(lib.hs2_qk_norm_rope), addr(lib.hs2_qk_norm_rope_bwd), addr(lib.hs2_qk_norm_rope_paged),
-                          addr(lib.hs2_page_table_update), addr(lib.hs2_paged_attn))
+                          addr(lib.hs2_page_table_update), addr(lib.hs2_paged_attn),
+                          addr(lib.hs2_stream_capturing))
     return mod
 
 
@@ -684,20 +688,27 @@ def _stream_workspace(nbytes: int, t: torch.Tensor, key: str, stream, ptr: int) 
     captured graph outlives the cache's choice of a buffer, so while capturing the caller gives one."""
     if not t.is_cuda:
         raise ValueError("the tensors must be CUDA tensors")
-    if stream is None:
-        capturing = torch.cuda.is_current_stream_capturing()
-    else:
-        with torch.cuda.stream(stream):
-            capturing = torch.cuda.is_current_stream_capturing()
-    if capturing:
+    if _fast.capturing(ptr):
         raise ValueError("give a workspace of your own while capturing a graph")
-    k = (t.device, key, ptr)
+    k = (t.get_device(), key, ptr)
     ws = _ws_cache.get(k)
     if ws is None or ws.numel() < nbytes:
         with _ws_lock, torch.cuda.device(t.device), torch.cuda.stream(stream):
             ws = torch.zeros(max(nbytes, 256), dtype=torch.uint8, device=t.device)
             _ws_cache[k] = ws
     return ws
+
+
+@functools.lru_cache(maxsize=4096)
+def _rope_bwd_bytes(device: int, T: int, Hq: int, Hk: int, d: int) -> int:
+    with torch.cuda.device(device):  # (the size goes by the device's number of SMs)
+        return qk_norm_rope_bwd_workspace_bytes(T, Hq, Hk, d)
+
+
+@functools.lru_cache(maxsize=4096)
+def _paged_attn_bytes(device: int, B: int, Hq: int, Hk: int, d: int) -> int:
+    with torch.cuda.device(device):
+        return paged_attn_workspace_bytes(B, Hq, Hk, d)
 
 
 def rope_frequencies(rot: int, base: float = 10000.0, *, scaling: str | None = None, factor: float = 1.0,
@@ -775,7 +786,7 @@ def qk_norm_rope_bwd(q, k, positions, inv_freq, dq_out, dk_out, *, q_weight=None
     st = _stream_on(stream, q)
     if workspace is None:
         heads = 0 if k is None else k.shape[-2] if k.dim() == q.dim() else 1
-        nbytes = qk_norm_rope_bwd_workspace_bytes(q.shape[:-2].numel(), q.shape[-2], heads, q.shape[-1])
+        nbytes = _rope_bwd_bytes(q.get_device(), q.shape[:-2].numel(), q.shape[-2], heads, q.shape[-1]) if q.is_cuda else 0
         workspace = _stream_workspace(nbytes, q, "rope_bwd", stream, st)
     _check(m.qk_norm_rope_bwd(q, k, positions, inv_freq, dq_out, dk_out, q_weight, k_weight, eps, interleaved, mscale, dq,
                               dk, dq_weight, dk_weight, workspace, st), "hs2_qk_norm_rope_bwd")
@@ -852,7 +863,7 @@ def paged_attn(q, k_pages, v_pages, page_table, lens, *, k_scale=None, v_scale=N
     st = _stream_on(stream, q)
     if workspace is None:
         heads = k_pages.shape[2] if k_pages.dim() == 4 else 1
-        nbytes = paged_attn_workspace_bytes(q.shape[0], q.shape[-2], heads, q.shape[-1])
+        nbytes = _paged_attn_bytes(q.get_device(), q.shape[0], q.shape[-2], heads, q.shape[-1]) if q.is_cuda else 0
         workspace = _stream_workspace(nbytes, q, "paged_attn", stream, st)
     _check(m.paged_attn(q, k_pages, v_pages, page_table, lens, f8, ks, vs, scale, window, out, lse, workspace, st),
            "hs2_paged_attn")
@@ -876,7 +887,7 @@ def cached_workspace(key: str, device=None, stream=None):
     ws = _ws_cache.get((device, key))
     if ws is None:
         stream = torch.cuda.current_stream(device) if stream is None else stream
-        ws = _ws_cache.get((device, key, stream.cuda_stream))
+        ws = _ws_cache.get((stream.device_index, key, stream.cuda_stream))
     return ws
 
 

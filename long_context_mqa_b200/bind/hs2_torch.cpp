@@ -111,12 +111,18 @@ RopePagedFn g_rope_paged = nullptr;
 TableFn g_table = nullptr;
 PagedFn g_paged = nullptr;
 
-void set_cache_entries(int64_t rope, int64_t rope_bwd, int64_t rope_paged, int64_t table, int64_t paged) {
+using CapturingFn = int (*)(void*);
+CapturingFn g_capturing = nullptr;
+bool capturing(int64_t stream) { return g_capturing(reinterpret_cast<void*>(stream)) != 0; }
+
+void set_cache_entries(int64_t rope, int64_t rope_bwd, int64_t rope_paged, int64_t table, int64_t paged,
+                       int64_t stream_capturing) {
   g_rope = reinterpret_cast<RopeFn>(rope);
   g_rope_bwd = reinterpret_cast<RopeBwdFn>(rope_bwd);
   g_rope_paged = reinterpret_cast<RopePagedFn>(rope_paged);
   g_table = reinterpret_cast<TableFn>(table);
   g_paged = reinterpret_cast<PagedFn>(paged);
+  g_capturing = reinterpret_cast<CapturingFn>(stream_capturing);
 }
 
 inline void need_on(const at::Tensor& t, const char* name, at::ScalarType dt, int64_t dim, const at::Tensor& like) {
@@ -373,6 +379,7 @@ int64_t paged_attn(const at::Tensor& q, const at::Tensor& k_pages, const at::Ten
 PYBIND11_MODULE(TORCH_EXTENSION_NAME, m) {
   m.def("set_entries", &set_entries);
   m.def("set_cache_entries", &set_cache_entries);
+  m.def("capturing", &capturing);
   m.def("qk_norm_rope", &qk_norm_rope);
   m.def("qk_norm_rope_bwd", &qk_norm_rope_bwd);
   m.def("qk_norm_rope_paged", &qk_norm_rope_paged);

@@ -5,6 +5,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <cudaTypedefs.h>
+#include <math.h>
 #include <stdint.h>
 
 #include <utility>
@@ -42,6 +43,9 @@ inline bool pool_strides_ok(const long long* s, int e4m3) {
     if (s[i] <= 0 || s[i] % unit != 0) return false;
   return true;
 }
+
+// Scale of an e4m3 cache: positive, finite, and so is its reciprocal.
+inline bool cache_scale_ok(float s) { return s > 0.f && s < HUGE_VALF && 1.f / s < HUGE_VALF; }
 
 // Launches `kernel` on `stream`; with pdl = true the launch may begin while the previous
 // kernel on the stream is still running (the kernel must call griddep_wait() before it reads

@@ -1000,6 +1000,15 @@ hs2_status hs2_bridge_kv_proj(const hs2_bf16* Hs, int T, int hidden, const hs2_b
                              reinterpret_cast<cudaStream_t>(stream));
 }
 
+int hs2_stream_capturing(hs2_stream stream) {
+  cudaStreamCaptureStatus s = cudaStreamCaptureStatusNone;
+  if (cudaStreamIsCapturing(reinterpret_cast<cudaStream_t>(stream), &s) != cudaSuccess) {
+    (void)cudaGetLastError();  // (the legacy stream while another one is captured)
+    return 1;
+  }
+  return s != cudaStreamCaptureStatusNone;
+}
+
 hs2_status hs2_read_device_status(const void* workspace, hs2_stream stream) {
   if (!workspace) return HS2_ERR_WORKSPACE;
   DevStatus h{};

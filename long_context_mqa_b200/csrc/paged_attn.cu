@@ -225,8 +225,9 @@ __global__ void __launch_bounds__(NT, 2) paged_attn_kernel(const __grid_constant
   // rows of Q and P without a head stay zero
   for (int i = tid; i < L::OFF_R / 16; i += NT) st_shared_v4(smem_u32(smem) + i * 16, 0u, 0u, 0u, 0u);
   fence_async_smem();
-  if (warp == 1) { tmem_alloc(&tmem_base, 256); tmem_relinquish(); }
   griddep_wait();
+  // (a kernel before this one may still be about to take its tensor memory until the wait ends)
+  if (warp == 1) { tmem_alloc(&tmem_base, 256); tmem_relinquish(); }
   griddep_launch_dependents();
 
   // ---- the line of tiles: each thread sums a run of sequences
@@ -806,13 +807,13 @@ hs2_status hs2_paged_attn(const hs2_bf16* Q, const void* K_pages, const void* V_
                           int max_pages, const int32_t* lens, int B, int Hq, int Hk, int d, int e4m3, float k_scale,
                           float v_scale, float scale, int window, hs2_bf16* out, float* lse, void* workspace,
                           size_t workspace_bytes, hs2_stream stream) {
-  if (!pattn_sizes_ok(B, Hq, Hk) || !Q || !K_pages || !V_pages || !k_page_strides || !v_page_strides || !page_table ||
-      !lens || !out || n_pages < 1 || page_size < 1 || max_pages < 1 || window < 0 ||
+  if (!pattn_sizes_ok(B, Hq, Hk) || !K_pages || !V_pages || !k_page_strides || !v_page_strides ||
+      (B > 0 && (!Q || !page_table || !lens || !out)) || n_pages < 1 || page_size < 1 || max_pages < 1 || window < 0 ||
       (long long)max_pages * page_size > 0x3FFFFFFFll || !(scale > 0.f && scale < INFINITY) || !aligned16(Q) ||
       !aligned16(K_pages) || !aligned16(V_pages) || !aligned16(out))
     return HS2_ERR_INVALID_ARG;
   if (!pool_strides_ok(k_page_strides, e4m3) || !pool_strides_ok(v_page_strides, e4m3)) return HS2_ERR_INVALID_ARG;
-  if (e4m3 && !(k_scale > 0.f && k_scale < INFINITY && v_scale > 0.f && v_scale < INFINITY)) return HS2_ERR_INVALID_ARG;
+  if (e4m3 && !(cache_scale_ok(k_scale) && cache_scale_ok(v_scale))) return HS2_ERR_INVALID_ARG;
   const int G = Hq / Hk;
   if (G > pattn::MH || page_size % 16 != 0 || (d != 128 && (d != 64 || e4m3)) || !device_is_sm100())
     return HS2_ERR_UNSUPPORTED_SHAPE;

@@ -503,6 +503,7 @@ static bool strides_ok(const void* p, long long ts, long long hs) {
   return aligned16(p) && ts >= 0 && hs >= 0 && ts % 8 == 0 && hs % 8 == 0;
 }
 static bool shape_ok(int d, int rot) { return (d == 64 || d == 128) && rot >= 16 && rot <= d && rot % 16 == 0; }
+static bool numbers_ok(float mscale, float eps) { return fabsf(mscale) < INFINITY && eps >= 0.f && eps < INFINITY; }
 static bool sizes_ok(int T, int Hq, int Hk) {
   return T >= 0 && Hq >= 1 && Hk >= 0 && Hq <= 1024 && Hk <= 1024;
 }
@@ -522,10 +523,11 @@ hs2_status hs2_qk_norm_rope(const hs2_bf16* Q, const hs2_bf16* K, long long q_to
                             const double* inv_freq, int T, int Hq, int Hk, int d, int rot, int interleaved,
                             float mscale, float eps, const void* q_weight, const void* k_weight, int weight_fp32,
                             hs2_bf16* q_out, hs2_bf16* k_out, hs2_stream stream) {
-  if (!rope::sizes_ok(T, Hq, Hk) || !Q || !positions || !inv_freq || !q_out || !aligned16(q_out) ||
-      !rope::strides_ok(Q, q_token_stride, q_head_stride) || !rope::weights_ok(q_weight, k_weight, Hk))
+  if (!rope::sizes_ok(T, Hq, Hk) || (T > 0 && (!Q || !positions || !q_out)) || !inv_freq || !aligned16(q_out) ||
+      !rope::strides_ok(Q, q_token_stride, q_head_stride) || !rope::weights_ok(q_weight, k_weight, Hk) ||
+      !rope::numbers_ok(mscale, eps))
     return HS2_ERR_INVALID_ARG;
-  if (Hk > 0 && (!K || !k_out || !aligned16(k_out) || !rope::strides_ok(K, k_token_stride, k_head_stride)))
+  if (Hk > 0 && ((T > 0 && (!K || !k_out)) || !aligned16(k_out) || !rope::strides_ok(K, k_token_stride, k_head_stride)))
     return HS2_ERR_INVALID_ARG;
   if (!rope::shape_ok(d, rot) || !device_is_sm100()) return HS2_ERR_UNSUPPORTED_SHAPE;
   if (T == 0) return HS2_OK;
@@ -554,15 +556,15 @@ hs2_status hs2_qk_norm_rope_paged(const hs2_bf16* Q, const hs2_bf16* K, const hs
                                   const long long* k_page_strides, const long long* v_page_strides, int n_pages,
                                   int page_size, int e4m3, float k_scale, float v_scale, void* workspace,
                                   size_t workspace_bytes, hs2_stream stream) {
-  if (!rope::sizes_ok(T, Hq, Hk) || Hk < 1 || !Q || !K || !V || !positions || !slots || !inv_freq || !q_out ||
-      !k_pages || !v_pages || !k_page_strides || !v_page_strides || n_pages < 1 || page_size < 1 ||
+  if (!rope::sizes_ok(T, Hq, Hk) || Hk < 1 || (T > 0 && (!Q || !K || !V || !positions || !slots || !q_out)) || !inv_freq ||
+      !rope::numbers_ok(mscale, eps) || !k_pages || !v_pages || !k_page_strides || !v_page_strides || n_pages < 1 || page_size < 1 ||
       (long long)n_pages * page_size > 0x7FFFFFFFll || !aligned16(q_out) || !aligned16(k_pages) ||
       !aligned16(v_pages) || !rope::strides_ok(Q, q_token_stride, q_head_stride) ||
       !rope::strides_ok(K, k_token_stride, k_head_stride) || !rope::strides_ok(V, v_token_stride, v_head_stride) ||
       !rope::weights_ok(q_weight, k_weight, Hk))
     return HS2_ERR_INVALID_ARG;
   if (!pool_strides_ok(k_page_strides, e4m3) || !pool_strides_ok(v_page_strides, e4m3)) return HS2_ERR_INVALID_ARG;
-  if (e4m3 && !(k_scale > 0.f && k_scale < INFINITY && v_scale > 0.f && v_scale < INFINITY)) return HS2_ERR_INVALID_ARG;
+  if (e4m3 && !(cache_scale_ok(k_scale) && cache_scale_ok(v_scale))) return HS2_ERR_INVALID_ARG;
   if (!rope::shape_ok(d, rot) || !device_is_sm100()) return HS2_ERR_UNSUPPORTED_SHAPE;
   if (!workspace || !aligned16(workspace) || workspace_bytes < rope::kStatusBytes) return HS2_ERR_WORKSPACE;
   if (T == 0) return HS2_OK;
@@ -601,11 +603,11 @@ hs2_status hs2_qk_norm_rope_bwd(const hs2_bf16* Q, const hs2_bf16* K, long long 
                                 const void* k_weight, int weight_fp32, const hs2_bf16* dq_out, const void* dk_out,
                                 int dk_out_fp32, hs2_bf16* dQ, hs2_bf16* dK, float* dq_weight, float* dk_weight,
                                 void* workspace, size_t workspace_bytes, hs2_stream stream) {
-  if (!rope::sizes_ok(T, Hq, Hk) || !Q || !positions || !inv_freq || !dq_out || !dQ || !aligned16(dq_out) ||
+  if (!rope::sizes_ok(T, Hq, Hk) || (T > 0 && (!Q || !positions || !dq_out || !dQ)) || !inv_freq || !aligned16(dq_out) ||
       !aligned16(dQ) || !rope::strides_ok(Q, q_token_stride, q_head_stride) ||
-      !rope::weights_ok(q_weight, k_weight, Hk))
+      !rope::weights_ok(q_weight, k_weight, Hk) || !rope::numbers_ok(mscale, eps))
     return HS2_ERR_INVALID_ARG;
-  if (Hk > 0 && (!K || !dk_out || !dK || !aligned16(dk_out) || !aligned16(dK) ||
+  if (Hk > 0 && ((T > 0 && (!K || !dk_out || !dK)) || !aligned16(dk_out) || !aligned16(dK) ||
                  !rope::strides_ok(K, k_token_stride, k_head_stride)))
     return HS2_ERR_INVALID_ARG;
   if (q_weight && (!dq_weight || (Hk > 0 && !dk_weight))) return HS2_ERR_INVALID_ARG;
