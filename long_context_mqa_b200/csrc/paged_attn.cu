@@ -316,7 +316,8 @@ __global__ void __launch_bounds__(NT, 2) paged_attn_kernel(const __grid_constant
       auto page_of = [&](int t) -> int {
         const int k0 = t * TILE + lane * p.box;
         if (lane >= n_box || k0 >= wk.len || k0 + p.box <= first) return kNoPage;
-        return __ldg(row_ids + k0 / p.page);
+        const int pg = __ldg(row_ids + k0 / p.page);
+        return pg == kNoPage ? -1 : pg;
       };
       auto checked = [&](int pg) -> int {
         if (pg >= 0 && pg < p.n_pages) return pg;

@@ -95,7 +95,8 @@ def paged_attn(q, k_pages, v_pages, table, lens, scale, window=0, ks=None, vs=No
     half a step of the second term, 2^-10, where the tile's largest probability counts 256: 2^-18 of it; a
     tile is 128 keys), then the output once more. A score is a sum of d products in 32 bits: 2^-16 of their
     absolute sum; an e4m3 cache's query elements are off by 2^-17 of the head's largest at most. 2^-13 for
-    exp2, the sums and the rescaling."""
+    exp2, the sums and the rescaling. A probability below 2^-126 of its row's largest, and an output below
+    2^-126, is no normal 32-bit (or bf16) number and may become zero: 2^-126 of each key's |v|, and 2^-126."""
     B, _, Hq, d = q.shape
     Hk, f8 = k_pages.shape[2], ks is not None
     out = torch.zeros(B, 1, Hq, d, dtype=torch.float64, device=q.device)
@@ -116,6 +117,7 @@ def paged_attn(q, k_pages, v_pages, table, lens, scale, window=0, ks=None, vs=No
         if f8:
             ds = ds + 2.0 ** -17 * qb.abs().amax(-1) * K.abs().sum(-1).amax(0)[:, None] * scale
         e = BF16 * o.abs() + (BF16 + 2.0 ** -13 + 2 * ds[..., None]) * A
+        e = e + 2.0 ** -126 * (1 + V.abs().sum(0)[:, None])
         if f8:
             tile = torch.div(at, 128, rounding_mode="floor") - first // 128
             most = torch.zeros(Hk, Hq // Hk, int(tile[-1]) + 1, dtype=torch.float64, device=q.device)
@@ -128,13 +130,14 @@ def paged_attn(q, k_pages, v_pages, table, lens, scale, window=0, ks=None, vs=No
 
 
 def page_table_step(table, lens, delta, ring, head, count, page, max_tokens):
-    """One request after the other (lists; table and ring are updated). Returns (lens, head, count, cu,
-    positions, slots)."""
-    cap, taken, back, cu, pos, slots = len(ring), 0, [], [0], [], []
+    """One request after the other (lists; table and ring are updated): none that needs pages is served after
+    one that the free list could not serve. Returns (lens, head, count, cu, positions, slots)."""
+    cap, taken, short, back, cu, pos, slots = len(ring), 0, False, [], [0], [], []
     new = []
     for b, (n, x) in enumerate(zip(lens, delta)):
         held, want = -(-n // page), -(-(n + x) // page)
-        ok = want <= held or want - held <= count - taken
+        short = short or want - held > count - taken
+        ok = want <= held or not short
         if want > held and ok:
             for j in range(held, want):
                 table[b][j] = ring[(head + taken) % cap]
