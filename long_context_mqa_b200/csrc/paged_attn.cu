@@ -15,10 +15,12 @@
 // below the row's (a cache with one dominant key).
 //
 // An e4m3 cache goes to the tensor core as it is (kind::f8f6f4; nothing is widened). The 16-bit
-// operand beside it is split into two e4m3 terms, hi = e4m3(x), lo = e4m3(x - hi), whose products
-// accumulate in the same accumulator: 4 + 4 significant bits, as many as a bf16 has. Q is first
-// scaled per head by a power of two so that its largest element lies in [128, 256) (elements down to
-// 2^-9 of it are exact, smaller ones are off by 2^-17 of it at most); P is scaled by 256.
+// operand beside it is split into two 8-bit terms whose products accumulate in the same accumulator.
+// P (scaled by 256): hi = e4m3(x), lo = e4m3(x - hi), 4 + 4 significant bits, as many as a bf16 has. Q, scaled
+// per head by a power of two so that its largest element lies in [2^10, 2^11): hi = e5m2(x), lo =
+// e4m3(x - hi). The first term leaves a multiple of 0 .. 16 of a bf16's last bit, which four bits hold, so an element
+// is exact down to 2^-12 of the largest, and off by 2^-20 of that at most below (e4m3 for both terms:
+// exact to 2^-9, off by 2^-17, which the logsumexp of a few keys showed: 7e-7 of it against 4e-8).
 //
 // The tiles of all (sequence, key head) pairs form one line that is cut into equal ranges, one per
 // CTA, from the lengths on the device (a captured launch serves any lengths). A pair that lies in one
@@ -100,9 +102,10 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, long l
   return __shfl_sync(0xffffffffu, ok, 0) != 0;
 }
 
-__host__ __device__ constexpr uint32_t idesc_e4m3(int M, int N, int a_mn, int b_mn) {
-  return (1u << 4) | ((uint32_t)(a_mn & 1) << 15) | ((uint32_t)(b_mn & 1) << 16) | ((uint32_t)(N >> 3) << 17) |
-         ((uint32_t)(M >> 4) << 24);  // D = f32, A and B = e4m3 (0)
+// A in e4m3, or in e5m2; B in e4m3
+__host__ __device__ constexpr uint32_t idesc_f8(int M, int N, int a_mn, int b_mn, int a_e5m2) {
+  return (1u << 4) | ((uint32_t)(a_e5m2 & 1) << 7) | ((uint32_t)(a_mn & 1) << 15) | ((uint32_t)(b_mn & 1) << 16) | ((uint32_t)(N >> 3) << 17) |
+         ((uint32_t)(M >> 4) << 24);  // D = f32; formats: e4m3 0, e5m2 1
 }
 __device__ __forceinline__ void umma_f8(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
   asm volatile(
@@ -117,6 +120,17 @@ __device__ __forceinline__ void split_e4m3(uint32_t x, uint32_t& hi, uint32_t& l
   uint32_t r;
   asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(h) : "r"(x));
   asm("{.reg .b32 w;\n\tcvt.rn.f16x2.e4m3x2 w, %1;\n\tsub.rn.f16x2 %0, %2, w;}" : "=r"(r) : "h"(h), "r"(x));
+  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(l) : "r"(r));
+  hi = h;
+  lo = l;
+}
+
+// the same with the first term in e5m2
+__device__ __forceinline__ void split_e5m2(uint32_t x, uint32_t& hi, uint32_t& lo) {
+  uint16_t h, l;
+  uint32_t r;
+  asm("cvt.rn.satfinite.e5m2x2.f16x2 %0, %1;" : "=h"(h) : "r"(x));
+  asm("{.reg .b32 w;\n\tcvt.rn.f16x2.e5m2x2 w, %1;\n\tsub.rn.f16x2 %0, %2, w;}" : "=r"(r) : "h"(h), "r"(x));
   asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(l) : "r"(r));
   hi = h;
   lo = l;
@@ -375,12 +389,12 @@ __global__ void __launch_bounds__(NT, 2) paged_attn_kernel(const __grid_constant
         tc_fence_after();
         const uint64_t ka = sdesc(smem_u32(sR + s * SLOT), 16, 1024);
         if constexpr (F8) {
-          constexpr uint32_t ID = idesc_e4m3(MH, TILE, 0, 0);
 #pragma unroll
           for (int h = 0; h < 2; ++h)  // Q's hi and lo terms
 #pragma unroll
             for (int kk = 0; kk < D / 32; ++kk)
-              umma_f8(tmem + tS, sdesc_at(qa, h * (MH * 128) + kk * 32), sdesc_at(ka, kk * 32), ID, h + kk > 0);
+              umma_f8(tmem + tS, sdesc_at(qa, h * (MH * 128) + kk * 32), sdesc_at(ka, kk * 32),
+                      idesc_f8(MH, TILE, 0, 0, h == 0), h + kk > 0);
         } else {
           constexpr uint32_t ID = idesc_bf16(MH, TILE, 0, 0);
 #pragma unroll
@@ -402,7 +416,7 @@ __global__ void __launch_bounds__(NT, 2) paged_attn_kernel(const __grid_constant
         tc_fence_after();
         const uint32_t pb = (jp & 1) * L::P_BYTES;
         if constexpr (F8) {
-          constexpr uint32_t ID = idesc_e4m3(MH, D, 0, 1);
+          constexpr uint32_t ID = idesc_f8(MH, D, 0, 1, 0);
           const uint64_t va = sdesc(smem_u32(sR + s * SLOT), TILE * 128, 1024);
 #pragma unroll
           for (int h = 0; h < 2; ++h)  // P's hi and lo terms
@@ -471,8 +485,8 @@ __global__ void __launch_bounds__(NT, 2) paged_attn_kernel(const __grid_constant
         }
         am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, 16));
         nan += __shfl_xor_sync(0xffffffffu, nan, 16);
-        // am 2^e in [128, 256)
-        int e = 134 - (int)(__float_as_uint(am) >> 23);  // 127 + 7 - biased exponent
+        // am 2^e in [2^10, 2^11)
+        int e = 137 - (int)(__float_as_uint(am) >> 23);  // 127 + 10 - biased exponent
         e = am > 0.f ? (e < -120 ? -120 : e > 120 ? 120 : e) : 0;
         const float up = __uint_as_float((uint32_t)(127 + e) << 23);
         c = p.c * __uint_as_float((uint32_t)(127 - e) << 23) + nan;
@@ -484,9 +498,9 @@ __global__ void __launch_bounds__(NT, 2) paged_attn_kernel(const __grid_constant
             const uint4& ww = w[i + k / 2];
             const uint32_t a = k % 2 ? ww.z : ww.x, b2 = k % 2 ? ww.w : ww.y;
             uint32_t h0, l0, h1, l1;
-            // (a bf16 element times a power of two below 256 is an f16 value, or too small to matter)
-            split_e4m3(pack_f16x2(__uint_as_float(a << 16) * up, __uint_as_float(a & 0xFFFF0000u) * up), h0, l0);
-            split_e4m3(pack_f16x2(__uint_as_float(b2 << 16) * up, __uint_as_float(b2 & 0xFFFF0000u) * up), h1, l1);
+            // (a bf16 element times that power of two is an f16 value, or too small to matter)
+            split_e5m2(pack_f16x2(__uint_as_float(a << 16) * up, __uint_as_float(a & 0xFFFF0000u) * up), h0, l0);
+            split_e5m2(pack_f16x2(__uint_as_float(b2 << 16) * up, __uint_as_float(b2 & 0xFFFF0000u) * up), h1, l1);
             hi[k] = h0 | (h1 << 16);
             lo[k] = l0 | (l1 << 16);
           }

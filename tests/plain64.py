@@ -94,7 +94,7 @@ def paged_attn(q, k_pages, v_pages, table, lens, scale, window=0, ks=None, vs=No
     Bounds. Every probability is rounded once: to bf16, or to two e4m3 terms (2^-4 times 2^-4 of the value, and
     half a step of the second term, 2^-10, where the tile's largest probability counts 256: 2^-18 of it; a
     tile is 128 keys), then the output once more. A score is a sum of d products in 32 bits: 2^-16 of their
-    absolute sum; an e4m3 cache's query elements are off by 2^-17 of the head's largest at most. 2^-13 for
+    absolute sum; an e4m3 cache's query elements are off by 2^-20 of the head's largest at most. 2^-13 for
     exp2, the sums and the rescaling. A probability below 2^-126 of its row's largest, and an output below
     2^-126, is no normal 32-bit (or bf16) number and may become zero: 2^-126 of each key's |v|, and 2^-126."""
     B, _, Hq, d = q.shape
@@ -115,7 +115,7 @@ def paged_attn(q, k_pages, v_pages, table, lens, scale, window=0, ks=None, vs=No
         A = torch.einsum("hgn,nhd->hgd", p, V.abs())
         ds = 2.0 ** -16 * torch.einsum("hgd,nhd->hgn", qb.abs(), K.abs()).amax(-1) * scale
         if f8:
-            ds = ds + 2.0 ** -17 * qb.abs().amax(-1) * K.abs().sum(-1).amax(0)[:, None] * scale
+            ds = ds + 2.0 ** -20 * qb.abs().amax(-1) * K.abs().sum(-1).amax(0)[:, None] * scale
         e = BF16 * o.abs() + (BF16 + 2.0 ** -13 + 2 * ds[..., None]) * A
         e = e + 2.0 ** -126 * (1 + V.abs().sum(0)[:, None])
         if f8:
