@@ -26,6 +26,8 @@
 // CTA, from the lengths on the device (a captured launch serves any lengths). A pair that lies in one
 // CTA's range is finished there; the others leave (m, l, acc) records that a second kernel joins in
 // the order of the ranges, so results do not vary from run to run.
+#include <type_traits>
+
 #include "host_util.h"
 #include "tc.cuh"
 
@@ -46,7 +48,7 @@ struct Params {
   int B, Hk, G, page, box, max_pages, n_pages, window;
   float c;       // scale log2(e), times K's scale
   float oscale;  // V's scale
-  int W;         // CTAs of the grid at most in use
+  int W;         // CTAs of the grid at most in use; of a cluster
   int4* cuts;    // [W] of the cut before each CTA's range: pair, first CTA of the pair, its segments (0: no cut in a pair)
   float* po;     // [W][2][G][D] records
   float2* pml;   // [W][2][G]
@@ -55,6 +57,7 @@ struct Params {
 };
 
 constexpr int MAX_NR = 5;
+constexpr int MAX_CS = 8;  // CTAs of a cluster at most
 struct Shared {
   uint64_t r_full[MAX_NR], r_empty[MAX_NR], q_ready, s_full, s_free, p_ready, o_full, drained;
   uint32_t tmem_base;
@@ -72,6 +75,8 @@ struct Lay {
   static constexpr int P_BYTES = MH * TILE * 2;
   static constexpr int NR = F8 || D == 64 ? 4 : 5;            // ring slots
   static constexpr int OFF_P = Q_BYTES, OFF_R = OFF_P + 2 * P_BYTES;  // (P of two tiles)
+  static constexpr int REC = D * 4 + 16;  // a row's accumulators in a cluster's join (16 bytes apart: banks)
+  static_assert(MH * (REC + 8) <= NR * SLOT, "a cluster's records lie in the ring");
   // the barriers lie behind the ring and nothing is declared beside it: 1,024-byte aligned without
   // slack, so that two CTAs with a fifth slot fit an SM
   static constexpr int OFF_B = OFF_R + NR * SLOT;
@@ -204,7 +209,24 @@ struct Split {
   }
 };
 
-template <int D, bool F8>
+// The one segment of a cluster's CTA.
+template <int TILE>
+struct One {
+  int b, hk, len, t0, n, off, cnt;
+  bool left;
+  __device__ __forceinline__ bool next(const Params&) {
+    const bool now = left;
+    left = false;
+    return now;
+  }
+  __device__ __forceinline__ int first_key(const Params& p) const {
+    return p.window > 0 && len > p.window ? len - p.window : 0;
+  }
+};
+
+// CL: short sequences. A cluster of p.W CTAs works on one (sequence, key head), its tiles shared out evenly,
+// and joins its accumulators through distributed shared memory: no line, no records, no second kernel.
+template <int D, bool F8, bool CL>
 __global__ void __launch_bounds__(NT, 2) paged_attn_kernel(const __grid_constant__ CUtensorMap tmK,
                                                            const __grid_constant__ CUtensorMap tmV, Params p) {
   using L = Lay<D, F8>;
@@ -244,57 +266,76 @@ __global__ void __launch_bounds__(NT, 2) paged_attn_kernel(const __grid_constant
   if (warp == 1) { tmem_alloc(&tmem_base, 256); tmem_relinquish(); }
   griddep_launch_dependents();
 
-  // ---- the line of tiles: each thread sums a run of sequences
-  const int per = (p.B + NT - 1) / NT;
-  int mine = 0;
-  bool bad = false;
-  for (int i = 0; i < per; ++i) {
-    const int b = tid * per + i;
-    int len, t0;
-    if (b < p.B) mine += pair_len(seq_tiles<TILE>(p, b, len, t0, &bad));
-  }
-  int x = mine;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int y = __shfl_up_sync(0xffffffffu, x, o);
-    if (lane >= o) x += y;
-  }
-  if (lane == 31) warp_sum[warp] = x;
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  int before = x - mine, all = 0;
-#pragma unroll
-  for (int w = 0; w < NT / 32; ++w) {
-    const int s = warp_sum[w];
-    if (w < warp) before += s;
-    all += s;
-  }
-  const int N = all * p.Hk, cta = blockIdx.x;
-  const Split split(N, p.W);
-  const int r0 = cta < split.W ? split.start(cta) : N, r1 = cta < split.W ? split.start(cta + 1) : N;
-  if (r0 < r1 && before * p.Hk <= r0 && r0 < (before + mine) * p.Hk) {
-    int at = before * p.Hk;
+  const int cta = blockIdx.x;
+  int r0 = 0;  // the start of this CTA's range on the line
+  Split split(1, 1);
+  std::conditional_t<CL, One<TILE>, Walk<TILE>> wk;
+  if constexpr (CL) {
+    const int rank = (int)cluster_ctarank(), pair = cta / p.W;
+    bool bad = false;
+    wk.b = pair / p.Hk; wk.hk = pair % p.Hk;
+    wk.n = seq_tiles<TILE>(p, wk.b, wk.len, wk.t0, &bad);
+    split = Split(wk.n, p.W);
+    wk.off = rank < split.W ? split.start(rank) : 0;
+    wk.cnt = rank < split.W ? split.start(rank + 1) - wk.off : 0;
+    wk.left = wk.cnt > 0;
+    if (bad && rank == 0 && tid == 0) report_status(p.st, kStatusBounds, 701);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+  } else {
+    // ---- the line of tiles: each thread sums a run of sequences
+    const int per = (p.B + NT - 1) / NT;
+    int mine = 0;
+    bool bad = false;
     for (int i = 0; i < per; ++i) {
       const int b = tid * per + i;
       int len, t0;
-      const int n = pair_len(seq_tiles<TILE>(p, b, len, t0));
-      if (r0 < at + n * p.Hk) {
-        const int hk = (r0 - at) / n;
-        s_start[0] = b; s_start[1] = at; s_start[2] = len; s_start[3] = t0; s_start[4] = hk; s_start[5] = at + hk * n;
-        break;
-      }
-      at += n * p.Hk;
+      if (b < p.B) mine += pair_len(seq_tiles<TILE>(p, b, len, t0, &bad));
     }
+    int x = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    if (lane == 31) warp_sum[warp] = x;
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    int before = x - mine, all = 0;
+#pragma unroll
+    for (int w = 0; w < NT / 32; ++w) {
+      const int s = warp_sum[w];
+      if (w < warp) before += s;
+      all += s;
+    }
+    const int N = all * p.Hk;
+    split = Split(N, p.W);
+    r0 = cta < split.W ? split.start(cta) : N;
+    const int r1 = cta < split.W ? split.start(cta + 1) : N;
+    if (r0 < r1 && before * p.Hk <= r0 && r0 < (before + mine) * p.Hk) {
+      int at = before * p.Hk;
+      for (int i = 0; i < per; ++i) {
+        const int b = tid * per + i;
+        int len, t0;
+        const int n = pair_len(seq_tiles<TILE>(p, b, len, t0));
+        if (r0 < at + n * p.Hk) {
+          const int hk = (r0 - at) / n;
+          s_start[0] = b; s_start[1] = at; s_start[2] = len; s_start[3] = t0; s_start[4] = hk; s_start[5] = at + hk * n;
+          break;
+        }
+        at += n * p.Hk;
+      }
+    }
+    if (bad && cta == 0) report_status(p.st, kStatusBounds, 701);
+    __syncthreads();
+    wk.pos = r0; wk.end = s_start[0] >= 0 ? r1 : r0;
+    wk.b = s_start[0]; wk.base = s_start[1]; wk.len = s_start[2]; wk.t0 = s_start[3];
+    wk.next_hk = s_start[4]; wk.at = s_start[5];
+    wk.n = wk.len > 0 ? (wk.len + TILE - 1) / TILE - wk.t0 : 0;
   }
-  if (bad && cta == 0) report_status(p.st, kStatusBounds, 701);
-  __syncthreads();
   const uint32_t tmem = tmem_base, tS = 0, tO = 128;
-  Walk<TILE> wk;
-  wk.pos = r0; wk.end = s_start[0] >= 0 ? r1 : r0;
-  wk.b = s_start[0]; wk.base = s_start[1]; wk.len = s_start[2]; wk.t0 = s_start[3];
-  wk.next_hk = s_start[4]; wk.at = s_start[5];
-  wk.n = wk.len > 0 ? (wk.len + TILE - 1) / TILE - wk.t0 : 0;
 
   if (warp == 0) {
     // ------------------------------------------------------------------ TMA producer: lane x loads
@@ -356,26 +397,31 @@ __global__ void __launch_bounds__(NT, 2) paged_attn_kernel(const __grid_constant
   } else if (warp == 1) {
     // ------------------------------------------------------------------ MMA issuer (one thread); before
     // the first tile can arrive the warp writes what the join has to know, and the rows of sequences without a key
-    if (lane == 1) {
-      int4 c = make_int4(0, 0, 0, 0);
-      if (s_start[0] >= 0) {
-        const int s = wk.at + OV;
-        if (r0 > s) {
-          c.x = wk.b * p.Hk + wk.next_hk;
-          c.y = split.owner(s);
-          c.z = split.owner(s + wk.n - 1) + 1 - c.y;
-        }
-      }
-      p.cuts[cta] = c;
-    }
-    for (int b = cta; b < p.B; b += gridDim.x) {
-      int len, t0;
-      if (seq_tiles<TILE>(p, b, len, t0) > 0) continue;
-      const int rows = p.Hk * p.G;
-      uint4* dst = reinterpret_cast<uint4*>(p.out + (size_t)b * rows * D);
+    auto zero = [&](size_t row0, int rows) {
+      uint4* dst = reinterpret_cast<uint4*>(p.out + row0 * D);
       for (int i = lane; i < rows * (D / 8); i += 32) dst[i] = make_uint4(0u, 0u, 0u, 0u);
       if (p.lse)
-        for (int i = lane; i < rows; i += 32) p.lse[(size_t)b * rows + i] = -INFINITY;
+        for (int i = lane; i < rows; i += 32) p.lse[row0 + i] = -INFINITY;
+    };
+    if constexpr (CL) {
+      if (wk.n == 0 && cta % p.W == 0) zero((size_t)(cta / p.W) * p.G, p.G);
+    } else {
+      if (lane == 1) {
+        int4 c = make_int4(0, 0, 0, 0);
+        if (s_start[0] >= 0) {
+          const int s = wk.at + OV;
+          if (r0 > s) {
+            c.x = wk.b * p.Hk + wk.next_hk;
+            c.y = split.owner(s);
+            c.z = split.owner(s + wk.n - 1) + 1 - c.y;
+          }
+        }
+        p.cuts[cta] = c;
+      }
+      for (int b = cta; b < p.B; b += gridDim.x) {
+        int len, t0;
+        if (seq_tiles<TILE>(p, b, len, t0) == 0) zero((size_t)b * p.Hk * p.G, p.Hk * p.G);
+      }
     }
     __syncwarp();
     if (lane == 0) {
@@ -651,12 +697,18 @@ __global__ void __launch_bounds__(NT, 2) paged_attn_kernel(const __grid_constant
                                   pack_bf16x2(acc[k + 4] * inv, acc[k + 5] * inv),
                                   pack_bf16x2(acc[k + 6] * inv, acc[k + 7] * inv));
         if (p.lse && lh == 0) p.lse[head] = (m_run + log2f(l_run)) * 0.69314718055994531f;
-      } else if (row < p.G) {  // a record: slot 1 where the segment begins its pair, else slot 0
-        const size_t rec = ((size_t)cta * 2 + (begins ? 1 : 0)) * p.G + row;
-        float4* dst = reinterpret_cast<float4*>(p.po + rec * D + o0);
+      } else if (row < p.G) {
+        float4* dst;
+        if constexpr (CL) {  // the ring is done with: its last product has been read
+          dst = reinterpret_cast<float4*>(sR + row * L::REC + o0 * 4);
+          if (lh == 0) reinterpret_cast<float2*>(sR + MH * L::REC)[row] = make_float2(m_run, l_run);
+        } else {  // a record: slot 1 where the segment begins its pair, else slot 0
+          const size_t rec = ((size_t)cta * 2 + (begins ? 1 : 0)) * p.G + row;
+          dst = reinterpret_cast<float4*>(p.po + rec * D + o0);
+          if (lh == 0) p.pml[rec] = make_float2(m_run, l_run);
+        }
 #pragma unroll
         for (int k = 0; k < OC; k += 4) dst[k / 4] = make_float4(acc[k], acc[k + 1], acc[k + 2], acc[k + 3]);
-        if (lh == 0) p.pml[rec] = make_float2(m_run, l_run);
       }
       c = c_next;
       __syncwarp();
@@ -665,6 +717,56 @@ __global__ void __launch_bounds__(NT, 2) paged_attn_kernel(const __grid_constant
   tc_fence_before();
   __syncthreads();
   if (warp == 1) { tc_fence_after(); tmem_dealloc(tmem, 256); }
+  if constexpr (CL) {
+    if (split.W == 1) return;  // (of the whole cluster)
+    __syncwarp();
+    cluster_sync_all();  // every CTA's accumulators are in its shared memory
+    // rows rank, rank + W, .. : a warp a row, every CTA's record of it asked for at once
+    constexpr int VL = D / 32;
+    const int rank = (int)cluster_ctarank();
+    for (int row = rank + p.W * warp; row < p.G; row += p.W * (NT / 32)) {
+      const uint32_t rec = smem_u32(sR) + row * L::REC + lane * (VL * 4), ml = smem_u32(sR) + MH * L::REC + row * 8;
+      float o[MAX_CS][VL], m[MAX_CS], l[MAX_CS];
+#pragma unroll
+      for (int i = 0; i < MAX_CS; ++i) {
+        m[i] = -INFINITY;
+        l[i] = 0.f;
+#pragma unroll
+        for (int v = 0; v < VL; ++v) o[i][v] = 0.f;
+        if (i < split.W) {
+          const uint32_t ra = dsmem_addr(rec, i), ma = dsmem_addr(ml, i);
+          m[i] = ld_dsmem_f32(ma);
+          l[i] = ld_dsmem_f32(ma + 4);
+          if constexpr (VL == 4) {
+            const float4 x = ld_dsmem_v4(ra);
+            o[i][0] = x.x; o[i][1] = x.y; o[i][2] = x.z; o[i][3] = x.w;
+          } else {
+            o[i][0] = ld_dsmem_f32(ra);
+            o[i][1] = ld_dsmem_f32(ra + 4);
+          }
+        }
+      }
+      float M = m[0], acc[VL], ls = 0.f;
+#pragma unroll
+      for (int i = 1; i < MAX_CS; ++i) M = fmaxf(M, m[i]);
+#pragma unroll
+      for (int v = 0; v < VL; ++v) acc[v] = 0.f;
+#pragma unroll
+      for (int i = 0; i < MAX_CS; ++i) {
+        const float w = m[i] == -INFINITY ? 0.f : fast_exp2(m[i] - M);
+        ls += l[i] * w;
+#pragma unroll
+        for (int v = 0; v < VL; ++v) acc[v] += o[i][v] * w;
+      }
+      const size_t head = (size_t)(wk.b * p.Hk + wk.hk) * p.G + row;
+      const float inv = ls == 0.f ? 0.f : p.oscale / ls;
+      uint32_t* dst = reinterpret_cast<uint32_t*>(p.out + head * D + lane * VL);
+#pragma unroll
+      for (int v = 0; v < VL; v += 2) dst[v / 2] = pack_bf16x2(acc[v] * inv, acc[v + 1] * inv);
+      if (lane == 0 && p.lse) p.lse[head] = (M + log2f(ls)) * 0.69314718055994531f;
+    }
+    cluster_sync_all();  // nothing reads another CTA's memory after this
+  }
 }
 
 // Joins the records of the (sequence, key head) pairs that several CTAs worked on, in the order of
@@ -789,15 +891,39 @@ static int gcd(int a, int b) { return b == 0 ? a : gcd(b, a % b); }
 template <int D, bool F8>
 static cudaError_t launch(const CUtensorMap& tk, const CUtensorMap& tv, const Params& p, cudaStream_t st) {
   using L = Lay<D, F8>;
-  cudaError_t e = cudaFuncSetAttribute(paged_attn_kernel<D, F8>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::BYTES);
+  const auto k = paged_attn_kernel<D, F8, false>;
+  cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, L::BYTES);
   if (e != cudaSuccess) return e;
   {
     LaunchScope ls("paged_attn", st);
-    e = launch_k(paged_attn_kernel<D, F8>, dim3(p.W), dim3(NT), L::BYTES, st, true, tk, tv, p);
+    e = launch_k(k, dim3(p.W), dim3(NT), L::BYTES, st, true, tk, tv, p);
   }
   if (e != cudaSuccess || p.W == 1) return e;
   LaunchScope ls("paged_join", st);
   return launch_k(paged_join_kernel<D>, dim3(p.W - 1, JX), dim3(JT), 0, st, true, p);
+}
+template <int D, bool F8>
+static cudaError_t launch_clusters(const CUtensorMap& tk, const CUtensorMap& tv, const Params& p, cudaStream_t st) {
+  using L = Lay<D, F8>;
+  const auto k = paged_attn_kernel<D, F8, true>;
+  cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, L::BYTES);
+  if (e != cudaSuccess) return e;
+  LaunchScope ls("paged_attn_cluster", st);
+  return launch_clusters_k(k, dim3(p.B * p.Hk * p.W), dim3(NT), L::BYTES, st, true, p.W, tk, tv, p);
+}
+
+// CTAs of a cluster for `pairs` (sequence, key head) of at most n tiles each; 0: the line of tiles.
+// Clusters spare the records and the second kernel, about five tiles' time, but share a pair's tiles among 8
+// CTAs at most, and a ragged batch's short pairs leave theirs idle (three quarters of the line's share
+// is what a batch of mixed lengths has to gain by). Measured, clusters and line: 64 heads on one key head, one
+// sequence of 1,000 tokens 8.3 and 10.8 us, of 4,096 13.3 and 10.5 us; 250 sequences of up to 1,000 tokens 21 and
+// 27 us, 16 of 8,192 24 and 21 us. Clusters of 16 gain nothing where these lose, and 16 of them take two waves.
+static int cluster_size(long long pairs, long long n, int sms) {
+  if (pairs > 2 * sms) return 0;
+  int cs = MAX_CS;
+  while (cs > 1 && (pairs * cs > 2 * sms || cs / 2 >= n)) cs /= 2;
+  const long long share = pairs * (n + OV) / (2 * sms);
+  return 4 * n <= cs * (20 + 3 * share) ? cs : 0;
 }
 
 }  // namespace pattn
@@ -846,11 +972,14 @@ hs2_status hs2_paged_attn(const hs2_bf16* Q, const void* K_pages, const void* V_
   p.wait_ns = wait_limit_ns();
   // tiles that the batch can have at most: one line of 32-bit tile numbers
   const long long span = (long long)max_pages * page_size;
-  const long long most = (long long)B * Hk * ((window > 0 && window < span ? window + tile : span) / tile + 1 + pattn::OV);
+  const long long n_max = window > 0 && window < span ? (window - 1) / tile + 2 : (span + tile - 1) / tile;  // of one pair
+  const long long most = (long long)B * Hk * (n_max + pattn::OV);
   if (most > 0x3FFFFFFFll) return HS2_ERR_UNSUPPORTED_SHAPE;
   p.W = 2 * num_sms();
   pattn::carve(&p, workspace, G, d, p.W);
-  if (most < p.W) p.W = (int)most;
+  const int cs = pattn::cluster_size((long long)B * Hk, n_max, num_sms());
+  if (cs > 0) p.W = cs;
+  else if (most < p.W) p.W = (int)most;
   CUtensorMap tk, tv;
   if (!make_tmap_pool(&tk, K_pages, d, page_size, Hk, n_pages, k_page_strides[0], k_page_strides[1], k_page_strides[2],
                       p.box, e4m3 != 0) ||
@@ -858,8 +987,13 @@ hs2_status hs2_paged_attn(const hs2_bf16* Q, const void* K_pages, const void* V_
                       p.box, e4m3 != 0))
     return HS2_ERR_CUDA;
   const cudaStream_t st = (cudaStream_t)stream;
-  const cudaError_t e = e4m3 ? pattn::launch<128, true>(tk, tv, p, st)
-                             : d == 128 ? pattn::launch<128, false>(tk, tv, p, st) : pattn::launch<64, false>(tk, tv, p, st);
+  cudaError_t e;
+  if (cs > 0)
+    e = e4m3 ? pattn::launch_clusters<128, true>(tk, tv, p, st)
+             : d == 128 ? pattn::launch_clusters<128, false>(tk, tv, p, st) : pattn::launch_clusters<64, false>(tk, tv, p, st);
+  else
+    e = e4m3 ? pattn::launch<128, true>(tk, tv, p, st)
+             : d == 128 ? pattn::launch<128, false>(tk, tv, p, st) : pattn::launch<64, false>(tk, tv, p, st);
   return e == cudaSuccess ? HS2_OK : HS2_ERR_CUDA;
 }
 
