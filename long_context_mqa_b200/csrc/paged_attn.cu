@@ -37,7 +37,7 @@ namespace pattn {
 constexpr int NT = 192;   // TMA warp, MMA warp, four softmax warps
 constexpr int MH = 64;    // MMA rows
 constexpr int kNoPage = -2147483647 - 1;
-constexpr int MIN_TILES = 1;  // a CTA's share at least
+constexpr int MIN_TILES = 2;  // a CTA's share of the line at least: a record costs about as much as a tile
 constexpr int OV = 2;         // what starting and ending a pair costs, in tiles
 
 struct Params {
@@ -51,7 +51,7 @@ struct Params {
   int W;         // CTAs of the grid at most in use; of a cluster
   int4* cuts;    // [W] of the cut before each CTA's range: pair, first CTA of the pair, its segments (0: no cut in a pair)
   float* po;     // [W][2][G][D] records
-  float2* pml;   // [W][2][G]
+  float2* pml;   // [G][W][2] their maxima and sums (a row's side by side: the join reads them a line at a time)
   long long wait_ns;
   DevStatus* st;
 };
@@ -197,8 +197,8 @@ struct Walk {
 // 64-bit w N / W cost the join as much as its records).
 struct Split {
   int W, q, r;
-  __device__ __forceinline__ Split(int N, int most) {
-    W = min(most, max((N + MIN_TILES - 1) / MIN_TILES, 1));
+  __device__ __forceinline__ Split(int N, int most, int least) {
+    W = min(most, max((N + least - 1) / least, 1));
     q = N / W;
     r = N - q * W;
   }
@@ -268,14 +268,14 @@ __global__ void __launch_bounds__(NT, 2) paged_attn_kernel(const __grid_constant
 
   const int cta = blockIdx.x;
   int r0 = 0;  // the start of this CTA's range on the line
-  Split split(1, 1);
+  Split split(1, 1, 1);
   std::conditional_t<CL, One<TILE>, Walk<TILE>> wk;
   if constexpr (CL) {
     const int rank = (int)cluster_ctarank(), pair = cta / p.W;
     bool bad = false;
     wk.b = pair / p.Hk; wk.hk = pair % p.Hk;
     wk.n = seq_tiles<TILE>(p, wk.b, wk.len, wk.t0, &bad);
-    split = Split(wk.n, p.W);
+    split = Split(wk.n, p.W, 1);
     wk.off = rank < split.W ? split.start(rank) : 0;
     wk.cnt = rank < split.W ? split.start(rank + 1) - wk.off : 0;
     wk.left = wk.cnt > 0;
@@ -311,7 +311,7 @@ __global__ void __launch_bounds__(NT, 2) paged_attn_kernel(const __grid_constant
       all += s;
     }
     const int N = all * p.Hk;
-    split = Split(N, p.W);
+    split = Split(N, p.W, MIN_TILES);
     r0 = cta < split.W ? split.start(cta) : N;
     const int r1 = cta < split.W ? split.start(cta + 1) : N;
     if (r0 < r1 && before * p.Hk <= r0 && r0 < (before + mine) * p.Hk) {
@@ -703,9 +703,9 @@ __global__ void __launch_bounds__(NT, 2) paged_attn_kernel(const __grid_constant
           dst = reinterpret_cast<float4*>(sR + row * L::REC + o0 * 4);
           if (lh == 0) reinterpret_cast<float2*>(sR + MH * L::REC)[row] = make_float2(m_run, l_run);
         } else {  // a record: slot 1 where the segment begins its pair, else slot 0
-          const size_t rec = ((size_t)cta * 2 + (begins ? 1 : 0)) * p.G + row;
-          dst = reinterpret_cast<float4*>(p.po + rec * D + o0);
-          if (lh == 0) p.pml[rec] = make_float2(m_run, l_run);
+          const size_t rec = (size_t)cta * 2 + (begins ? 1 : 0);
+          dst = reinterpret_cast<float4*>(p.po + (rec * p.G + row) * D + o0);
+          if (lh == 0) p.pml[(size_t)row * (2 * p.W) + rec] = make_float2(m_run, l_run);
         }
 #pragma unroll
         for (int k = 0; k < OC; k += 4) dst[k / 4] = make_float4(acc[k], acc[k + 1], acc[k + 2], acc[k + 3]);
@@ -770,105 +770,114 @@ __global__ void __launch_bounds__(NT, 2) paged_attn_kernel(const __grid_constant
 }
 
 // Joins the records of the (sequence, key head) pairs that several CTAs worked on, in the order of
-// their ranges. A pair cut into cnt segments has cnt - 1 cuts inside it, and the JX blocks of each such cut join every
-// JX (cnt - 1)th of its head rows: all blocks have about G / JX records to read, however the line is cut.
-// What bounds it is the chain of dependent reads, each a microsecond's third from L2: the main kernel
-// leaves what a cut's blocks have to know in one 16-byte word, and a row's maxima, sums and accumulators are
-// asked for together. Warps that a block has to spare share a row's records.
+// their ranges. A pair cut into cnt segments has cnt - 1 cuts inside it, and the JX blocks of each such cut share
+// the pair's units, whole head rows or 32 columns of one (where there are more blocks than rows: one sequence of
+// 256k tokens has 64 rows of 296 records), so all blocks have about as much to read however the line is
+// cut. What bounds it is the chain of dependent reads, each a microsecond's third from L2: the main
+// kernel leaves what a cut's blocks have to know in one 16-byte word, and a unit's maxima, sums and
+// accumulators are asked for together. Warps that a block has to spare share a unit's records.
 constexpr int JT = 256, JW = JT / 32, JX = 2;
+// A unit: 4 LR columns of a head row; LR lanes read a record, 32 / LR records at a time.
+template <int D, int LR>
+__device__ __forceinline__ void join_units(const Params& p, int pair, int w0, int cnt, int first, int step,
+                                           float (*s_acc)[D]) {
+  constexpr int RPL = 32 / LR, C = D / (4 * LR), U = 4, ML = 5;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane / LR, li = lane % LR;
+  const int units = p.G * C, mine = first < units ? (units - first + step - 1) / step : 0;
+  const int split = mine >= 8 ? 1 : mine >= 4 ? 2 : mine >= 2 ? 4 : 8, sub = warp % split;
+  for (int k0 = 0; k0 < mine; k0 += JW / split) {
+    const int k = k0 + warp / split, unit = first + k * step, row = unit / C, col = (unit % C) * (4 * LR) + li * 4;
+    const bool on = k < mine;
+    // the first segment begins its pair (record 1 of its CTA), the others begin their CTA's range
+    auto rec = [&](int i) { return (w0 + i) * 2 + (i == 0 ? 1 : 0); };
+    const float2* ml = p.pml + (size_t)row * (2 * p.W);
+    float acc[4] = {0.f, 0.f, 0.f, 0.f}, l = 0.f, M = -INFINITY;
+    auto weight = [&](float x, float to) { return x == -INFINITY ? 0.f : fast_exp2(x - to); };
+    if (on) {
+      float4 o[U];
+      float m[U];
+      auto load = [&](int i0) {  // this lane's records i0, i0 + split * RPL, ..
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const int i = i0 + u * (split * RPL);
+          m[u] = -INFINITY;
+          o[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (i < cnt) {
+            const int r = rec(i);
+            o[u] = __ldcg(reinterpret_cast<const float4*>(p.po + ((size_t)r * p.G + row) * D + col));
+            m[u] = __ldcg(&ml[r].x);
+          }
+        }
+      };
+      const int i_first = sub * RPL + g;
+      load(i_first);
+      // maxima and sums, ML records a lane at a time
+      for (int i0 = lane; i0 - lane < cnt; i0 += 32 * ML) {
+        float2 x[ML];
+        float top = M;
+#pragma unroll
+        for (int j = 0; j < ML; ++j)
+          x[j] = i0 + 32 * j < cnt ? __ldcg(ml + rec(i0 + 32 * j)) : make_float2(-INFINITY, 0.f);
+#pragma unroll
+        for (int j = 0; j < ML; ++j) top = fmaxf(top, x[j].x);
+        l *= weight(M, top);
+#pragma unroll
+        for (int j = 0; j < ML; ++j) l += x[j].y * weight(x[j].x, top);
+        M = top;
+      }
+      float top = M;
+#pragma unroll
+      for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+      l *= weight(M, top);
+      M = top;
+#pragma unroll
+      for (int d = 16; d > 0; d >>= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
+      for (int i0 = i_first;;) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const float w = weight(m[u], M);
+          acc[0] += o[u].x * w; acc[1] += o[u].y * w; acc[2] += o[u].z * w; acc[3] += o[u].w * w;
+        }
+        i0 += U * split * RPL;
+        if (i0 - g >= cnt) break;  // (the same for every lane)
+        load(i0);
+      }
+#pragma unroll
+      for (int d = 16; d >= LR; d >>= 1)
+#pragma unroll
+        for (int v = 0; v < 4; ++v) acc[v] += __shfl_xor_sync(0xffffffffu, acc[v], d);
+    }
+    if (split > 1) {
+      __syncthreads();
+      if (g == 0) *reinterpret_cast<float4*>(&s_acc[warp][li * 4]) = make_float4(acc[0], acc[1], acc[2], acc[3]);
+      __syncthreads();
+      if (sub == 0 && g == 0)
+        for (int j = 1; j < split; ++j) {
+          const float4 x = *reinterpret_cast<const float4*>(&s_acc[warp + j][li * 4]);
+          acc[0] += x.x; acc[1] += x.y; acc[2] += x.z; acc[3] += x.w;
+        }
+    }
+    if (on && sub == 0 && g == 0) {
+      const size_t head = (size_t)pair * p.G + row;
+      const float inv = l == 0.f ? 0.f : p.oscale / l;
+      *reinterpret_cast<uint2*>(p.out + head * D + col) =
+          make_uint2(pack_bf16x2(acc[0] * inv, acc[1] * inv), pack_bf16x2(acc[2] * inv, acc[3] * inv));
+      if (col == 0 && p.lse) p.lse[head] = (M + log2f(l)) * 0.69314718055994531f;
+    }
+  }
+}
 template <int D>
 __global__ void __launch_bounds__(JT, 4) paged_join_kernel(Params p) {
-  constexpr int VL = D / 32, U = 4;  // columns of a lane, records in flight
-  __shared__ float s_acc[JW][D];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, cut = blockIdx.x + 1;
+  __shared__ __align__(16) float s_acc[JW][D];
+  const int cut = blockIdx.x + 1;
   griddep_wait();
   griddep_launch_dependents();
   const int4 c = __ldcg(p.cuts + cut);
   const int pair = c.x, w0 = c.y, cnt = c.z;
   if (cnt == 0) return;  // not between two tiles of a pair
   const int step = JX * (cnt - 1), first = (cut - w0 - 1) * JX + blockIdx.y;
-  const int rows = first < p.G ? (p.G - first + step - 1) / step : 0;
-  const int split = rows >= 8 ? 1 : rows >= 4 ? 2 : rows >= 2 ? 4 : 8, sub = warp % split;
-  for (int k0 = 0; k0 < rows; k0 += JW / split) {
-    const int k = k0 + warp / split, row = first + k * step;
-    const bool on = k < rows;
-    // the first segment begins its pair (record 1 of its CTA), the others begin their CTA's range
-    auto rec = [&](int i) { return ((size_t)(w0 + i) * 2 + (i == 0 ? 1 : 0)) * p.G + row; };
-    float acc[VL], l = 0.f, M = -INFINITY;
-#pragma unroll
-    for (int i = 0; i < VL; ++i) acc[i] = 0.f;
-    if (on) {
-      float o[U][VL], m[U];
-      auto load = [&](int i0) {  // records i0, i0 + split, ..
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-          const int i = i0 + u * split;
-          m[u] = -INFINITY;
-#pragma unroll
-          for (int v = 0; v < VL; ++v) o[u][v] = 0.f;
-          if (i < cnt) {
-            const size_t r = rec(i);
-            const float* src = p.po + r * D + lane * VL;
-            if constexpr (VL == 4) {
-              const float4 x = __ldcg(reinterpret_cast<const float4*>(src));
-              o[u][0] = x.x; o[u][1] = x.y; o[u][2] = x.z; o[u][3] = x.w;
-            } else {
-              const float2 x = __ldcg(reinterpret_cast<const float2*>(src));
-              o[u][0] = x.x; o[u][1] = x.y;
-            }
-            m[u] = __ldcg(&p.pml[r].x);
-          }
-        }
-      };
-      // maxima and sums of the first 64 records, a lane two; there are rarely more
-      const float2 none = make_float2(-INFINITY, 0.f);
-      const float2 m0 = lane < cnt ? __ldcg(&p.pml[rec(lane)]) : none;
-      const float2 m1 = lane + 32 < cnt ? __ldcg(&p.pml[rec(lane + 32)]) : none;
-      load(sub);
-      M = fmaxf(m0.x, m1.x);
-      for (int i = lane + 64; i < cnt; i += 32) M = fmaxf(M, __ldcg(&p.pml[rec(i)]).x);
-#pragma unroll
-      for (int d = 16; d > 0; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
-      auto weight = [&](float x) { return x == -INFINITY ? 0.f : fast_exp2(x - M); };
-      l = m0.y * weight(m0.x) + m1.y * weight(m1.x);
-      for (int i = lane + 64; i < cnt; i += 32) {
-        const float2 ml = __ldcg(&p.pml[rec(i)]);
-        l += ml.y * weight(ml.x);
-      }
-#pragma unroll
-      for (int d = 16; d > 0; d >>= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
-      for (int i0 = sub;;) {
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-          const float w = weight(m[u]);
-#pragma unroll
-          for (int v = 0; v < VL; ++v) acc[v] += o[u][v] * w;
-        }
-        i0 += U * split;
-        if (i0 >= cnt) break;
-        load(i0);
-      }
-    }
-    if (split > 1) {
-      __syncthreads();
-#pragma unroll
-      for (int v = 0; v < VL; ++v) s_acc[warp][lane * VL + v] = acc[v];
-      __syncthreads();
-      if (sub == 0)
-        for (int j = 1; j < split; ++j) {
-#pragma unroll
-          for (int v = 0; v < VL; ++v) acc[v] += s_acc[warp + j][lane * VL + v];
-        }
-    }
-    if (on && sub == 0) {
-      const size_t head = (size_t)pair * p.G + row;
-      const float inv = l == 0.f ? 0.f : p.oscale / l;
-      uint32_t* dst = reinterpret_cast<uint32_t*>(p.out + head * D + lane * VL);
-#pragma unroll
-      for (int v = 0; v < VL; v += 2) dst[v / 2] = pack_bf16x2(acc[v] * inv, acc[v + 1] * inv);
-      if (lane == 0 && p.lse) p.lse[head] = (M + log2f(l)) * 0.69314718055994531f;
-    }
-  }
+  if (step > 2 * p.G) join_units<D, 8>(p, pair, w0, cnt, first, step, s_acc);
+  else join_units<D, D / 4>(p, pair, w0, cnt, first, step, s_acc);
 }
 
 // -------------------------------------------------------------------------------------- host
