@@ -677,23 +677,30 @@ def _marshal():
     return _fast
 
 
-def _stream_on(stream, t: torch.Tensor) -> int:
-    if stream is not None and stream.device != t.device:
-        raise ValueError(f"the stream is on {stream.device}, the tensors on {t.device}")
-    return _stream_ptr(stream, t) if t.is_cuda else 0  # (a host tensor fails the checks in C++)
-
-
-def _stream_workspace(nbytes: int, t: torch.Tensor, key: str, stream, ptr: int) -> torch.Tensor:
-    """The cached workspace of (device, op, stream): calls on different streams do not share one. A
-    captured graph outlives the cache's choice of a buffer, so while capturing the caller gives one."""
-    if not t.is_cuda:
+def _stream_of(t: torch.Tensor) -> int:
+    """The cudaStream_t of the current stream of t's device."""
+    dev = t.get_device()
+    if dev < 0:
         raise ValueError("the tensors must be CUDA tensors")
-    if _fast.capturing(ptr):
-        raise ValueError("give a workspace of your own while capturing a graph")
+    return _raw_stream(dev) if _raw_stream is not None else torch.cuda.current_stream(dev).cuda_stream
+
+
+def _on_stream(stream, t: torch.Tensor):
+    """The context of a call with stream=...: what the call allocates belongs to that stream too."""
+    if stream.device_index != t.get_device():
+        raise ValueError(f"the stream is on {stream.device}, the tensors on {t.device}")
+    return torch.cuda.stream(stream)
+
+
+def _stream_workspace(nbytes: int, t: torch.Tensor, key: str, ptr: int) -> torch.Tensor:
+    """The cached workspace of (device, op, stream): calls on different streams do not share one. (The
+    marshalling module refuses it while the stream is being captured: the caller gives one then.)"""
     k = (t.get_device(), key, ptr)
     ws = _ws_cache.get(k)
     if ws is None or ws.numel() < nbytes:
-        with _ws_lock, torch.cuda.device(t.device), torch.cuda.stream(stream):
+        if lib.hs2_stream_capturing(ptr):
+            raise ValueError("give a workspace of your own while capturing a graph")
+        with _ws_lock, torch.cuda.device(t.device):
             ws = torch.zeros(max(nbytes, 256), dtype=torch.uint8, device=t.device)
             _ws_cache[k] = ws
     return ws
@@ -754,12 +761,16 @@ def qk_norm_rope(q, k, positions, inv_freq, *, q_weight=None, k_weight=None, eps
     float64 (rope_frequencies); q_weight, k_weight [d] bf16 or float32, both or neither (no norm).
     Returns (q_out, k_out), bf16, contiguous, shaped like q and k.
     """
+    if stream is not None:
+        with _on_stream(stream, q):
+            return qk_norm_rope(q, k, positions, inv_freq, q_weight=q_weight, k_weight=k_weight, eps=eps,
+                                interleaved=interleaved, mscale=mscale, q_out=q_out, k_out=k_out)
     m = _marshal()
     q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device) if q_out is None else q_out
     if k is not None and k_out is None:
         k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
     _check(m.qk_norm_rope(q, k, positions, inv_freq, q_weight, k_weight, eps, interleaved, mscale, q_out, k_out,
-                          _stream_on(stream, q)), "hs2_qk_norm_rope")
+                          _stream_of(q)), "hs2_qk_norm_rope")
     return q_out, k_out
 
 
@@ -775,6 +786,11 @@ def qk_norm_rope_bwd(q, k, positions, inv_freq, dq_out, dk_out, *, q_weight=None
 
     Returns (dq, dk, dq_weight, dk_weight): bf16 shaped like q and k, float32 [d] (None without weights).
     """
+    if stream is not None:
+        with _on_stream(stream, q):
+            return qk_norm_rope_bwd(q, k, positions, inv_freq, dq_out, dk_out, q_weight=q_weight, k_weight=k_weight,
+                                    eps=eps, interleaved=interleaved, mscale=mscale, dq=dq, dk=dk, dq_weight=dq_weight,
+                                    dk_weight=dk_weight, workspace=workspace)
     m = _marshal()
     new = lambda t: torch.empty(t.shape, dtype=torch.bfloat16, device=t.device)
     dq = new(q) if dq is None else dq
@@ -783,13 +799,14 @@ def qk_norm_rope_bwd(q, k, positions, inv_freq, dq_out, dk_out, *, q_weight=None
         dq_weight = torch.empty(q.shape[-1], dtype=torch.float32, device=q.device)
     if k_weight is not None and dk_weight is None:
         dk_weight = torch.empty(q.shape[-1], dtype=torch.float32, device=q.device)
-    st = _stream_on(stream, q)
-    if workspace is None:
+    st = _stream_of(q)
+    kept = workspace is None
+    if kept:
         heads = 0 if k is None else k.shape[-2] if k.dim() == q.dim() else 1
-        nbytes = _rope_bwd_bytes(q.get_device(), q.shape[:-2].numel(), q.shape[-2], heads, q.shape[-1]) if q.is_cuda else 0
-        workspace = _stream_workspace(nbytes, q, "rope_bwd", stream, st)
+        nbytes = _rope_bwd_bytes(q.get_device(), q.shape[:-2].numel(), q.shape[-2], heads, q.shape[-1])
+        workspace = _stream_workspace(nbytes, q, "rope_bwd", st)
     _check(m.qk_norm_rope_bwd(q, k, positions, inv_freq, dq_out, dk_out, q_weight, k_weight, eps, interleaved, mscale, dq,
-                              dk, dq_weight, dk_weight, workspace, st), "hs2_qk_norm_rope_bwd")
+                              dk, dq_weight, dk_weight, workspace, kept, st), "hs2_qk_norm_rope_bwd")
     return dq, dk, dq_weight, dk_weight
 
 
@@ -807,15 +824,25 @@ def qk_norm_rope_paged(q, k, v, positions, slots, k_pages, v_pages, inv_freq, *,
 
     A token with a negative slot is padding: nothing of it is read or written. Returns q_out.
     """
+    if stream is not None:
+        with _on_stream(stream, q):
+            return qk_norm_rope_paged(q, k, v, positions, slots, k_pages, v_pages, inv_freq, q_weight=q_weight,
+                                      k_weight=k_weight, eps=eps, interleaved=interleaved, mscale=mscale, k_scale=k_scale,
+                                      v_scale=v_scale, q_out=q_out, workspace=workspace)
     m = _marshal()
     f8, ks, vs = _scales(k_scale, v_scale)
     q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device) if q_out is None else q_out
-    st = _stream_on(stream, q)
-    if workspace is None:
-        workspace = _stream_workspace(256, q, "rope_paged", stream, st)
+    st = _stream_of(q)
+    kept = workspace is None
+    if kept:
+        workspace = _stream_workspace(256, q, "rope_paged", st)
     _check(m.qk_norm_rope_paged(q, k, v, positions, slots, k_pages, v_pages, inv_freq, q_weight, k_weight, eps,
-                                interleaved, mscale, f8, ks, vs, q_out, workspace, st), "hs2_qk_norm_rope_paged")
+                                interleaved, mscale, f8, ks, vs, q_out, workspace, kept, st), "hs2_qk_norm_rope_paged")
     return q_out
+
+
+def _new_i32(like: torch.Tensor, n: int) -> torch.Tensor:
+    return torch.empty(n, dtype=torch.int32, device=like.device)
 
 
 def page_table_update(page_table, lens, delta, free_ring, free_state, page_size, max_tokens, *, lens_out=None,
@@ -827,18 +854,23 @@ def page_table_update(page_table, lens, delta, free_ring, free_state, page_size,
     place; lens_out and free_state_out may be lens and free_state themselves (they are new tensors otherwise).
     Returns (lens_out, free_state_out, cu_tokens [B+1], positions [max_tokens], slots [max_tokens]).
     """
+    if stream is not None:
+        with _on_stream(stream, page_table):
+            return page_table_update(page_table, lens, delta, free_ring, free_state, page_size, max_tokens,
+                                     lens_out=lens_out, free_state_out=free_state_out, cu_tokens=cu_tokens,
+                                     positions=positions, slots=slots, workspace=workspace)
     m = _marshal()
-    new = lambda n: torch.empty(n, dtype=torch.int32, device=page_table.device)
-    lens_out = new(lens.shape) if lens_out is None else lens_out
-    free_state_out = new(2) if free_state_out is None else free_state_out
-    cu_tokens = new(lens.shape[0] + 1) if cu_tokens is None else cu_tokens
-    positions = new(max_tokens) if positions is None else positions
-    slots = new(max_tokens) if slots is None else slots
-    st = _stream_on(stream, page_table)
-    if workspace is None:
-        workspace = _stream_workspace(256, page_table, "page_table", stream, st)
+    lens_out = _new_i32(lens, lens.shape[0]) if lens_out is None else lens_out
+    free_state_out = _new_i32(lens, 2) if free_state_out is None else free_state_out
+    cu_tokens = _new_i32(lens, lens.shape[0] + 1) if cu_tokens is None else cu_tokens
+    positions = _new_i32(lens, max_tokens) if positions is None else positions
+    slots = _new_i32(lens, max_tokens) if slots is None else slots
+    st = _stream_of(page_table)
+    kept = workspace is None
+    if kept:
+        workspace = _stream_workspace(256, page_table, "page_table", st)
     _check(m.page_table_update(page_table, lens, delta, free_ring, free_state, page_size, max_tokens, lens_out,
-                               free_state_out, cu_tokens, positions, slots, workspace, st), "hs2_page_table_update")
+                               free_state_out, cu_tokens, positions, slots, workspace, kept, st), "hs2_page_table_update")
     return lens_out, free_state_out, cu_tokens, positions, slots
 
 
@@ -855,17 +887,22 @@ def paged_attn(q, k_pages, v_pages, page_table, lens, *, k_scale=None, v_scale=N
     tokens that are seen (0: all). Returns (out [B,1,Hq,d] bf16, lse [B,1,Hq] float32); an empty sequence gives
     zeros and -infinity.
     """
+    if stream is not None:
+        with _on_stream(stream, q):
+            return paged_attn(q, k_pages, v_pages, page_table, lens, k_scale=k_scale, v_scale=v_scale, scale=scale,
+                              window=window, out=out, lse=lse, workspace=workspace)
     m = _marshal()
     f8, ks, vs = _scales(k_scale, v_scale)
     scale = 1.0 / math.sqrt(q.shape[-1]) if scale is None else float(scale)
     out = torch.empty_like(q) if out is None else out
     lse = torch.empty(q.shape[:-1], dtype=torch.float32, device=q.device) if lse is None else lse
-    st = _stream_on(stream, q)
-    if workspace is None:
+    st = _stream_of(q)
+    kept = workspace is None
+    if kept:
         heads = k_pages.shape[2] if k_pages.dim() == 4 else 1
-        nbytes = _paged_attn_bytes(q.get_device(), q.shape[0], q.shape[-2], heads, q.shape[-1]) if q.is_cuda else 0
-        workspace = _stream_workspace(nbytes, q, "paged_attn", stream, st)
-    _check(m.paged_attn(q, k_pages, v_pages, page_table, lens, f8, ks, vs, scale, window, out, lse, workspace, st),
+        nbytes = _paged_attn_bytes(q.get_device(), q.shape[0], q.shape[-2], heads, q.shape[-1])
+        workspace = _stream_workspace(nbytes, q, "paged_attn", st)
+    _check(m.paged_attn(q, k_pages, v_pages, page_table, lens, f8, ks, vs, scale, window, out, lse, workspace, kept, st),
            "hs2_paged_attn")
     return out, lse
 

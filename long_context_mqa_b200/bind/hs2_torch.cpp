@@ -113,7 +113,6 @@ PagedFn g_paged = nullptr;
 
 using CapturingFn = int (*)(void*);
 CapturingFn g_capturing = nullptr;
-bool capturing(int64_t stream) { return g_capturing(reinterpret_cast<void*>(stream)) != 0; }
 
 void set_cache_entries(int64_t rope, int64_t rope_bwd, int64_t rope_paged, int64_t table, int64_t paged,
                        int64_t stream_capturing) {
@@ -214,7 +213,11 @@ void* out_of(const at::Tensor& o, const char* name, at::ScalarType dt, const at:
   HS2_ARG_CHECK(o.sizes() == shape.sizes(), name, " must be shaped ", shape.sizes(), ", got ", o.sizes());
   return o.data_ptr();
 }
-void need_ws(const at::Tensor& ws, const at::Tensor& like) {
+// kept: the binding's own workspace of the stream. A captured graph would outlive the binding's choice of a
+// buffer, and two graphs would share it.
+void need_ws(const at::Tensor& ws, const at::Tensor& like, bool kept, int64_t stream) {
+  HS2_ARG_CHECK(!kept || g_capturing(reinterpret_cast<void*>(stream)) == 0,
+                "give a workspace of your own while capturing a graph");
   HS2_ARG_CHECK(ws.is_cuda() && ws.is_contiguous(), "workspace must be a contiguous CUDA tensor");
   HS2_ARG_CHECK(ws.device() == like.device(), "workspace is on ", ws.device(), ", not on ", like.device());
 }
@@ -236,7 +239,7 @@ int64_t qk_norm_rope(const at::Tensor& q, const OptT& k, const at::Tensor& posit
 int64_t qk_norm_rope_bwd(const at::Tensor& q, const OptT& k, const at::Tensor& positions, const at::Tensor& inv_freq,
                          const at::Tensor& dq_out, const OptT& dk_out, const OptT& qw, const OptT& kw, double eps,
                          bool interleaved, double mscale, const at::Tensor& dq, const OptT& dk, const OptT& dqw,
-                         const OptT& dkw, const at::Tensor& ws, int64_t stream) {
+                         const OptT& dkw, const at::Tensor& ws, bool kept, int64_t stream) {
   const RopeArgs a = rope_args(q, k, positions, inv_freq, qw, kw);
   const void* gq = out_of(dq_out, "dq_out", at::kBFloat16, q);
   void* xq = out_of(dq, "dq", at::kBFloat16, q);
@@ -259,7 +262,7 @@ int64_t qk_norm_rope_bwd(const at::Tensor& q, const OptT& k, const at::Tensor& p
     need_on(*dkw, "dk_weight", at::kFloat, 1, q);
     HS2_ARG_CHECK(dkw->size(0) == a.d, "dk_weight must have ", a.d, " elements");
   }
-  need_ws(ws, q);
+  need_ws(ws, q, kept, stream);
   c10::DeviceGuard guard(q.device());
   return g_rope_bwd(a.q.p, a.k.p, a.q.ts, a.q.hs, a.k.ts, a.k.hs, a.pos, a.freq, a.T, a.Hq, a.Hk, a.d, a.rot, interleaved,
                     (float)mscale, (float)eps, a.qw, a.kw, a.f32, gq, gk, g32, xq, xk,
@@ -299,7 +302,7 @@ int64_t qk_norm_rope_paged(const at::Tensor& q, const at::Tensor& k, const at::T
                            const at::Tensor& slots, const at::Tensor& k_pages, const at::Tensor& v_pages,
                            const at::Tensor& inv_freq, const OptT& qw, const OptT& kw, double eps, bool interleaved,
                            double mscale, bool f8, double k_scale, double v_scale, const at::Tensor& q_out,
-                           const at::Tensor& ws, int64_t stream) {
+                           const at::Tensor& ws, bool kept, int64_t stream) {
   const RopeArgs a = rope_args(q, k, positions, inv_freq, qw, kw);
   const Rows vr = rows_of(v, "v", q.dim() - 2, q);
   HS2_ARG_CHECK(vr.H == a.Hk && vr.d == a.d, "v must be shaped like k");
@@ -308,7 +311,7 @@ int64_t qk_norm_rope_paged(const at::Tensor& q, const at::Tensor& k, const at::T
   void* qo = out_of(q_out, "q_out", at::kBFloat16, q);
   const Pool kp = pool_of(k_pages, "k_pages", f8, q), vp = pool_of(v_pages, "v_pages", f8, q);
   HS2_ARG_CHECK(same_shape(kp, vp) && kp.H == a.Hk && kp.d == a.d, "k_pages and v_pages must be [n_pages, page, Hk, d]");
-  need_ws(ws, q);
+  need_ws(ws, q, kept, stream);
   c10::DeviceGuard guard(q.device());
   return g_rope_paged(a.q.p, a.k.p, vr.p, a.q.ts, a.q.hs, a.k.ts, a.k.hs, vr.ts, vr.hs, a.pos, slots.data_ptr<int32_t>(),
                       a.freq, a.T, a.Hq, a.Hk, a.d, a.rot, interleaved, (float)mscale, (float)eps, a.qw, a.kw, a.f32, qo,
@@ -320,7 +323,7 @@ int64_t qk_norm_rope_paged(const at::Tensor& q, const at::Tensor& k, const at::T
 int64_t page_table_update(const at::Tensor& table, const at::Tensor& lens, const at::Tensor& delta,
                           const at::Tensor& ring, const at::Tensor& state, int64_t page, int64_t max_tokens,
                           const at::Tensor& lens_out, const at::Tensor& state_out, const at::Tensor& cu,
-                          const at::Tensor& positions, const at::Tensor& slots, const at::Tensor& ws, int64_t stream) {
+                          const at::Tensor& positions, const at::Tensor& slots, const at::Tensor& ws, bool kept, int64_t stream) {
   need(table, "page_table", at::kInt, 2);
   const int64_t B = table.size(0);
   need_on(lens, "lens", at::kInt, 1, table);
@@ -336,7 +339,7 @@ int64_t page_table_update(const at::Tensor& table, const at::Tensor& lens, const
   HS2_ARG_CHECK(state.size(0) == 2 && state_out.size(0) == 2, "free_state must hold the ring's head and count");
   HS2_ARG_CHECK(cu.size(0) == B + 1, "cu_tokens must be [B + 1]");
   HS2_ARG_CHECK(positions.size(0) == max_tokens && slots.size(0) == max_tokens, "positions and slots must be [max_tokens]");
-  need_ws(ws, table);
+  need_ws(ws, table, kept, stream);
   c10::DeviceGuard guard(table.device());
   return g_table(table.data_ptr<int32_t>(), fits(B, "B"), fits(table.size(1), "max_pages"), lens.data_ptr<int32_t>(),
                  delta.data_ptr<int32_t>(), ring.data_ptr<int32_t>(), fits(ring.size(0), "the ring's size"),
@@ -349,7 +352,7 @@ int64_t page_table_update(const at::Tensor& table, const at::Tensor& lens, const
 // hs2_paged_attn
 int64_t paged_attn(const at::Tensor& q, const at::Tensor& k_pages, const at::Tensor& v_pages, const at::Tensor& table,
                    const at::Tensor& lens, bool f8, double k_scale, double v_scale, double scale, int64_t window,
-                   const at::Tensor& out, const OptT& lse, const at::Tensor& ws, int64_t stream) {
+                   const at::Tensor& out, const OptT& lse, const at::Tensor& ws, bool kept, int64_t stream) {
   need(q, "q", at::kBFloat16, 4);
   const int64_t B = q.size(0), Hq = q.size(2), d = q.size(3);
   HS2_ARG_CHECK(q.size(1) == 1, "q must be [B, 1, Hq, d], got ", q.sizes());
@@ -366,7 +369,7 @@ int64_t paged_attn(const at::Tensor& q, const at::Tensor& k_pages, const at::Ten
     HS2_ARG_CHECK(lse->size(0) == B && lse->size(1) == 1 && lse->size(2) == Hq, "lse must be [B, 1, Hq]");
     l = lse->data_ptr<float>();
   }
-  need_ws(ws, q);
+  need_ws(ws, q, kept, stream);
   c10::DeviceGuard guard(q.device());
   return g_paged(q.data_ptr(), kp.p, vp.p, kp.strides, vp.strides, fits(kp.n, "n_pages"), fits(kp.page, "page size"),
                  table.data_ptr<int32_t>(), fits(table.size(1), "max_pages"), lens.data_ptr<int32_t>(), fits(B, "B"),
@@ -379,7 +382,6 @@ int64_t paged_attn(const at::Tensor& q, const at::Tensor& k_pages, const at::Ten
 PYBIND11_MODULE(TORCH_EXTENSION_NAME, m) {
   m.def("set_entries", &set_entries);
   m.def("set_cache_entries", &set_cache_entries);
-  m.def("capturing", &capturing);
   m.def("qk_norm_rope", &qk_norm_rope);
   m.def("qk_norm_rope_bwd", &qk_norm_rope_bwd);
   m.def("qk_norm_rope_paged", &qk_norm_rope_paged);
