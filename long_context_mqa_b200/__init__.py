@@ -21,7 +21,6 @@ h [T, hidden] bf16, w [n_layers, 2, hidden, d] bf16 -> kv [n_layers, 2, T, d] bf
 from __future__ import annotations
 
 import ctypes
-import functools
 import math
 import os
 import threading
@@ -692,7 +691,7 @@ def _on_stream(stream, t: torch.Tensor):
     return torch.cuda.stream(stream)
 
 
-def _stream_workspace(nbytes: int, t: torch.Tensor, key: str, ptr: int) -> torch.Tensor:
+def _stream_workspace(t: torch.Tensor, key: str, ptr: int, nbytes: int = 256) -> torch.Tensor:
     """The cached workspace of (device, op, stream): calls on different streams do not share one. (The
     marshalling module refuses it while the stream is being captured: the caller gives one then.)"""
     k = (t.get_device(), key, ptr)
@@ -701,21 +700,9 @@ def _stream_workspace(nbytes: int, t: torch.Tensor, key: str, ptr: int) -> torch
         if lib.hs2_stream_capturing(ptr):
             raise ValueError("give a workspace of your own while capturing a graph")
         with _ws_lock, torch.cuda.device(t.device):
-            ws = torch.zeros(max(nbytes, 256), dtype=torch.uint8, device=t.device)
+            ws = torch.zeros(nbytes, dtype=torch.uint8, device=t.device)
             _ws_cache[k] = ws
     return ws
-
-
-@functools.lru_cache(maxsize=4096)
-def _rope_bwd_bytes(device: int, T: int, Hq: int, Hk: int, d: int) -> int:
-    with torch.cuda.device(device):  # (the size goes by the device's number of SMs)
-        return qk_norm_rope_bwd_workspace_bytes(T, Hq, Hk, d)
-
-
-@functools.lru_cache(maxsize=4096)
-def _paged_attn_bytes(device: int, B: int, Hq: int, Hk: int, d: int) -> int:
-    with torch.cuda.device(device):
-        return paged_attn_workspace_bytes(B, Hq, Hk, d)
 
 
 def rope_frequencies(rot: int, base: float = 10000.0, *, scaling: str | None = None, factor: float = 1.0,
@@ -802,11 +789,16 @@ def qk_norm_rope_bwd(q, k, positions, inv_freq, dq_out, dk_out, *, q_weight=None
     st = _stream_of(q)
     kept = workspace is None
     if kept:
+        workspace = _stream_workspace(q, "rope_bwd", st)
+    call = lambda ws: m.qk_norm_rope_bwd(q, k, positions, inv_freq, dq_out, dk_out, q_weight, k_weight, eps, interleaved,
+                                         mscale, dq, dk, dq_weight, dk_weight, ws, kept, st)
+    code = call(workspace)
+    if code == ERR_WORKSPACE and kept:  # (the first call of this size)
         heads = 0 if k is None else k.shape[-2] if k.dim() == q.dim() else 1
-        nbytes = _rope_bwd_bytes(q.get_device(), q.shape[:-2].numel(), q.shape[-2], heads, q.shape[-1])
-        workspace = _stream_workspace(nbytes, q, "rope_bwd", st)
-    _check(m.qk_norm_rope_bwd(q, k, positions, inv_freq, dq_out, dk_out, q_weight, k_weight, eps, interleaved, mscale, dq,
-                              dk, dq_weight, dk_weight, workspace, kept, st), "hs2_qk_norm_rope_bwd")
+        with torch.cuda.device(q.device):  # (the size goes by the device's number of SMs)
+            nbytes = qk_norm_rope_bwd_workspace_bytes(q.shape[:-2].numel(), q.shape[-2], heads, q.shape[-1])
+        code = call(_stream_workspace(q, "rope_bwd", st, nbytes))
+    _check(code, "hs2_qk_norm_rope_bwd")
     return dq, dk, dq_weight, dk_weight
 
 
@@ -835,7 +827,7 @@ def qk_norm_rope_paged(q, k, v, positions, slots, k_pages, v_pages, inv_freq, *,
     st = _stream_of(q)
     kept = workspace is None
     if kept:
-        workspace = _stream_workspace(256, q, "rope_paged", st)
+        workspace = _stream_workspace(q, "rope_paged", st)
     _check(m.qk_norm_rope_paged(q, k, v, positions, slots, k_pages, v_pages, inv_freq, q_weight, k_weight, eps,
                                 interleaved, mscale, f8, ks, vs, q_out, workspace, kept, st), "hs2_qk_norm_rope_paged")
     return q_out
@@ -868,7 +860,7 @@ def page_table_update(page_table, lens, delta, free_ring, free_state, page_size,
     st = _stream_of(page_table)
     kept = workspace is None
     if kept:
-        workspace = _stream_workspace(256, page_table, "page_table", st)
+        workspace = _stream_workspace(page_table, "page_table", st)
     _check(m.page_table_update(page_table, lens, delta, free_ring, free_state, page_size, max_tokens, lens_out,
                                free_state_out, cu_tokens, positions, slots, workspace, kept, st), "hs2_page_table_update")
     return lens_out, free_state_out, cu_tokens, positions, slots
@@ -899,11 +891,15 @@ def paged_attn(q, k_pages, v_pages, page_table, lens, *, k_scale=None, v_scale=N
     st = _stream_of(q)
     kept = workspace is None
     if kept:
+        workspace = _stream_workspace(q, "paged_attn", st)
+    call = lambda ws: m.paged_attn(q, k_pages, v_pages, page_table, lens, f8, ks, vs, scale, window, out, lse, ws, kept, st)
+    code = call(workspace)
+    if code == ERR_WORKSPACE and kept:  # (the first call of this size)
         heads = k_pages.shape[2] if k_pages.dim() == 4 else 1
-        nbytes = _paged_attn_bytes(q.get_device(), q.shape[0], q.shape[-2], heads, q.shape[-1])
-        workspace = _stream_workspace(nbytes, q, "paged_attn", st)
-    _check(m.paged_attn(q, k_pages, v_pages, page_table, lens, f8, ks, vs, scale, window, out, lse, workspace, kept, st),
-           "hs2_paged_attn")
+        with torch.cuda.device(q.device):  # (the size goes by the device's number of SMs)
+            nbytes = paged_attn_workspace_bytes(q.shape[0], q.shape[-2], heads, q.shape[-1])
+        code = call(_stream_workspace(q, "paged_attn", st, nbytes))
+    _check(code, "hs2_paged_attn")
     return out, lse
 
 

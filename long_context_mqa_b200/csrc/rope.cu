@@ -459,11 +459,12 @@ constexpr int ANGLE = 8;
 static int parts_of(int T, int passes, int warps) {
   long long best = 0;
   int parts = 1;
-  for (int n = 1; n <= passes; ++n) {
-    const long long waves = ((long long)T * n + warps - 1) / warps;
-    const long long cost = waves * ((passes + n - 1) / n + ANGLE);
+  for (int n = 1;;) {  // the fewest warps for each number of passes a warp
+    const int per = (passes + n - 1) / n;
+    const long long waves = ((long long)T * n + warps - 1) / warps, cost = waves * (per + ANGLE);
     if (n == 1 || cost < best) { best = cost; parts = n; }
-    if (n >= 64 && waves > 1) break;
+    if (per == 1) break;
+    n = (passes + per - 2) / (per - 1);
   }
   return parts;
 }
