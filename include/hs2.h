@@ -450,7 +450,8 @@ HS2_API hs2_status hs2_page_table_update(int32_t* page_table, int B, int max_pag
  *      as 0) are recorded as HS2_ERR_DEVICE_BOUNDS
  * scale  positive and finite
  * out [B, 1, Hq, d] bf16; lse [B, 1, Hq] fp32 natural log, or NULL
- * The split of the work depends on the lengths only, and partial results are joined in a fixed order.
+ * The split of the work depends on the lengths and the call's sizes only, and partial results are joined in
+ * a fixed order: results do not vary from run to run.
  * Supported: d = 128, or d = 64 with a bf16 cache; Hq / Hk <= 64; page_size % 16 == 0. Workspace:
  * hs2_paged_attn_workspace_bytes.
  */

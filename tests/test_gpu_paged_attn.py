@@ -96,9 +96,9 @@ def test_pool_without_a_head_dimension(hs2, f8):
 
 
 @pytest.mark.parametrize("B,n,Hq,Hk,f8", [(1, 40000, 64, 1, False), (2, 70001, 8, 1, True), (200, 300, 16, 2, False),
-                                          (1025, 40, 4, 4, True)])
+                                          (1025, 40, 4, 4, True), (150, 200, 4, 1, False), (280, 100, 3, 1, True)])
 def test_long_and_many(hs2, B, n, Hq, Hk, f8):
-    """Pairs cut into many ranges, many pairs in one range, and more sequences than threads."""
+    """Pairs cut into many ranges, many pairs in one range, more sequences than threads, and a block a pair."""
     c = Cache([n - (37 * b) % n for b in range(B)], Hq, Hk, 128, 64, f8)
     c.check(c.run(hs2))
 
@@ -179,6 +179,32 @@ def test_bad_pages_and_lengths_are_recorded(hs2):
             ws.zero_()
 
 
+@pytest.mark.parametrize("f8", [False, True])
+def test_pages_before_the_window_may_be_gone(hs2, f8):
+    """Table entries of pages that lie wholly before the window are not read."""
+    c = Cache([700, 129, 40], 8, 2, 128, 16, f8)
+    c.table[0, :(700 - 150) // 16] = -1
+    c.check(c.run(hs2, window=150), 150)
+    assert hs2.read_device_status(hs2.cached_workspace("paged_attn")) == 0
+
+
+def test_without_logsumexp(hs2):
+    """The C entry takes lse NULL."""
+    import ctypes
+    for lens in ([700, 0, 5], [30000, 0, 5]):
+        c = Cache(lens, 6, 2, 64, 16)
+        want = c.run(hs2)[0]
+        out = torch.empty_like(want)
+        ws = torch.zeros(hs2.paged_attn_workspace_bytes(3, 6, 2, 64), dtype=torch.uint8, device="cuda")
+        st = (ctypes.c_longlong * 3)(*c.k.stride()[:3])
+        code = hs2.lib.hs2_paged_attn(c.q.data_ptr(), c.k.data_ptr(), c.v.data_ptr(), st, st, c.k.shape[0], 16,
+                                      c.table.data_ptr(), c.table.shape[1], c.l.data_ptr(), 3, 6, 2, 64, 0, 1.0, 1.0,
+                                      1 / math.sqrt(64), 0, out.data_ptr(), None, ws.data_ptr(), ws.nbytes,
+                                      torch.cuda.current_stream().cuda_stream)
+        assert code == hs2.OK and hs2.read_device_status(ws) == 0
+        assert torch.equal(out, want)
+
+
 def test_offsets_past_32_bits(hs2):
     """Pages whose rows start beyond 2^31 elements of the pool."""
     n, page, d = 140000, 128, 128
@@ -193,9 +219,10 @@ def test_offsets_past_32_bits(hs2):
     c.check(c.run(hs2))
 
 
-def test_streams_graphs_and_new_lengths(hs2):
-    """Two streams at once, and two captured calls replayed with other lengths, queries and table entries."""
-    c = Cache([900, 40, 0, 1500], 16, 2, 128, 32)
+@pytest.mark.parametrize("times", [1, 12])  # (clusters; the line of tiles and its join)
+def test_streams_graphs_and_new_lengths(hs2, times):
+    """Two streams at once, and two captured calls replayed with other lengths and queries."""
+    c = Cache([900 * times, 40, 0, 1500 * times], 16, 2, 128, 32)
     want = c.run(hs2)
     s = [torch.cuda.Stream() for _ in range(2)]
     for x in s:
@@ -213,6 +240,7 @@ def test_streams_graphs_and_new_lengths(hs2):
             out = c.run(hs2, workspace=ws)
         graphs.append((gr, ws, out))
     for lens in ([900, 40, 0, 1500], [1, 0, 0, 1400], [0, 0, 0, 0], [899, 33, 0, 2]):
+        lens = [n * times if n > 100 else n for n in lens]
         c.lens = lens
         c.l.copy_(torch.tensor(lens, dtype=torch.int32))
         c.q.mul_(-0.75)
