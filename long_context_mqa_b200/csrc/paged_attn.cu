@@ -698,7 +698,7 @@ __global__ void __launch_bounds__(NT, 2) paged_attn_kernel(const __grid_constant
       const float c_next = more ? load_q(wk.b * p.Hk + wk.hk) : 0.f;
       if (!add_o()) break;
       l_run += __shfl_xor_sync(0xffffffffu, l_run, 16);
-      if (row < p.G && whole) {
+      if (whole && row < p.G) {
         const size_t head = (size_t)pair * p.G + row;
         const float inv = l_run == 0.f ? 0.f : p.oscale / l_run;
         uint4* dst = reinterpret_cast<uint4*>(p.out + head * D + o0);
@@ -708,18 +708,33 @@ __global__ void __launch_bounds__(NT, 2) paged_attn_kernel(const __grid_constant
                                   pack_bf16x2(acc[k + 4] * inv, acc[k + 5] * inv),
                                   pack_bf16x2(acc[k + 6] * inv, acc[k + 7] * inv));
         if (p.lse && lh == 0) p.lse[head] = (m_run + log2f(l_run)) * 0.69314718055994531f;
-      } else if (row < p.G) {
-        float4* dst;
+      } else if (!whole) {
         if constexpr (CL) {  // the ring is done with: its last product has been read
-          dst = reinterpret_cast<float4*>(sR + row * L::REC + o0 * 4);
-          if (lh == 0) reinterpret_cast<float2*>(sR + MH * L::REC)[row] = make_float2(m_run, l_run);
-        } else {  // a record: slot 1 where the segment begins its pair, else slot 0
-          const size_t rec = (size_t)cta * 2 + (begins ? 1 : 0);
-          dst = reinterpret_cast<float4*>(p.po + (rec * p.G + row) * D + o0);
-          if (lh == 0) p.pml[(size_t)row * (2 * p.W) + rec] = make_float2(m_run, l_run);
-        }
+          float4* dst = reinterpret_cast<float4*>(sR + row * L::REC + o0 * 4);
 #pragma unroll
-        for (int k = 0; k < OC; k += 4) dst[k / 4] = make_float4(acc[k], acc[k + 1], acc[k + 2], acc[k + 3]);
+          for (int k = 0; k < OC; k += 4) dst[k / 4] = make_float4(acc[k], acc[k + 1], acc[k + 2], acc[k + 3]);
+          if (lh == 0) reinterpret_cast<float2*>(sR + MH * L::REC)[row] = make_float2(m_run, l_run);
+        } else {
+          // a record: slot 1 where the segment begins its pair, else slot 0. 128 bytes of a row at a time, through
+          // the warp's own rows of the two P buffers (a lane's 16 bytes of its row each cost a line: 2 us at the end)
+          const size_t rec = (size_t)cta * 2 + (begins ? 1 : 0);
+#pragma unroll
+          for (int j = 0; j < NO; ++j) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              *reinterpret_cast<float4*>(sP + lh * L::P_BYTES + sw128_off(row, k)) =
+                  make_float4(acc[j * 32 + 4 * k], acc[j * 32 + 4 * k + 1], acc[j * 32 + 4 * k + 2], acc[j * 32 + 4 * k + 3]);
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const int h = i / 4, r = qd * 16 + (i % 4) * 4 + lane / 8, ch = lane % 8;
+              const float4 v = *reinterpret_cast<const float4*>(sP + h * L::P_BYTES + sw128_off(r, ch));
+              if (r < p.G) *reinterpret_cast<float4*>(p.po + (rec * p.G + r) * D + h * OC + j * 32 + ch * 4) = v;
+            }
+            __syncwarp();
+          }
+          if (row < p.G && lh == 0) p.pml[(size_t)row * (2 * p.W) + rec] = make_float2(m_run, l_run);
+        }
       }
       c = c_next;
       __syncwarp();
