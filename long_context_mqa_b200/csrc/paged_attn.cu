@@ -60,7 +60,7 @@ struct Params {
   float c;       // scale log2(e), times K's scale
   float oscale;  // V's scale
   int W;         // CTAs of the grid at most in use; of a cluster
-  int4* cuts;    // [W] of the cut before each CTA's range: pair, first CTA of the pair, its segments (0: no cut in a pair)
+  int4* cuts;    // [W] of the cut before each CTA's range: pair, its first CTA, its segments (0: no cut in a pair)
   float* po;     // [W][2][G][D] records
   float2* pml;   // [G][W][2] their maxima and sums (a row's side by side: the join reads them a line at a time)
   long long wait_ns;
@@ -69,6 +69,7 @@ struct Params {
 
 constexpr int MAX_NR = 5;
 constexpr int MAX_CS = 8;  // CTAs of a cluster at most
+constexpr int FEW = 256;   // keys: above, the roundings of P average out (and two terms cost a tenth of the time)
 struct Shared {
   uint64_t r_full[MAX_NR], r_empty[MAX_NR], q_ready, s_full, s_free, p_ready, o_full, drained;
   uint32_t tmem_base;
@@ -76,16 +77,21 @@ struct Shared {
   int warp_sum[NT / 32], start[6];
 };
 
-template <int D, bool F8>
+// CL: the clusters of short sequences. Where a head sees few keys they hold P in two bf16 terms (e4m3 has two
+// anyway), 16 significant bits, for one rounding of each to bf16 shows there (a head with two keys: 0.0027 of the
+// output instead of 0.0016; from 256 keys on 0.0019 and less).
+template <int D, bool F8, bool CL>
 struct Lay {
   static constexpr int TILE = F8 || D == 64 ? 128 : 64;       // keys of a tile: 16 KB of K
   static constexpr int EB = F8 ? 1 : 2;
   static constexpr int NKB = D * EB / 128;                    // 128-byte column blocks of a cache row
   static constexpr int SLOT = TILE * D * EB;
   static constexpr int Q_BYTES = MH * D * 2;                  // (e4m3: hi and lo terms)
-  static constexpr int P_BYTES = MH * TILE * 2;
-  static constexpr int NR = F8 || D == 64 ? 4 : 5;            // ring slots
-  static constexpr int OFF_P = Q_BYTES, OFF_R = OFF_P + 2 * P_BYTES;  // (P of two tiles)
+  static constexpr int P_BYTES = MH * TILE * 2;               // one term of P (e4m3: both)
+  static constexpr bool TWO = CL && !F8;
+  static constexpr int NB = TWO && D == 64 ? 1 : 2, PB = P_BYTES * (TWO ? 2 : 1);  // buffers of P, one's bytes
+  static constexpr int NR = F8 || D == 64 || CL ? 4 : 5;      // ring slots
+  static constexpr int OFF_P = Q_BYTES, OFF_R = OFF_P + NB * PB;
   static constexpr int REC = D * 4 + 16;  // a row's accumulators in a cluster's join (16 bytes apart: banks)
   static_assert(MH * (REC + 8) <= NR * SLOT, "a cluster's records lie in the ring");
   // the barriers lie behind the ring and nothing is declared beside it: 1,024-byte aligned without
@@ -120,8 +126,8 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, long l
 
 // A in e4m3, or in e5m2; B in e4m3
 __host__ __device__ constexpr uint32_t idesc_f8(int M, int N, int a_mn, int b_mn, int a_e5m2) {
-  return (1u << 4) | ((uint32_t)(a_e5m2 & 1) << 7) | ((uint32_t)(a_mn & 1) << 15) | ((uint32_t)(b_mn & 1) << 16) | ((uint32_t)(N >> 3) << 17) |
-         ((uint32_t)(M >> 4) << 24);  // D = f32; formats: e4m3 0, e5m2 1
+  return (1u << 4) | ((uint32_t)(a_e5m2 & 1) << 7) | ((uint32_t)(a_mn & 1) << 15) | ((uint32_t)(b_mn & 1) << 16) |
+         ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);  // D = f32; formats: e4m3 0, e5m2 1
 }
 __device__ __forceinline__ void umma_f8(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
   asm volatile(
@@ -240,7 +246,7 @@ struct One {
 template <int D, bool F8, bool CL>
 __global__ void __launch_bounds__(NT, 2) paged_attn_kernel(const __grid_constant__ CUtensorMap tmK,
                                                            const __grid_constant__ CUtensorMap tmV, Params p) {
-  using L = Lay<D, F8>;
+  using L = Lay<D, F8, CL>;
   constexpr int TILE = L::TILE, NR = L::NR, NKB = L::NKB, SLOT = L::SLOT;
   extern __shared__ __align__(1024) uint8_t smem[];
   uint8_t *sQ = smem, *sP = smem + L::OFF_P, *sR = smem + L::OFF_R;
@@ -347,6 +353,7 @@ __global__ void __launch_bounds__(NT, 2) paged_attn_kernel(const __grid_constant
     wk.n = wk.len > 0 ? (wk.len + TILE - 1) / TILE - wk.t0 : 0;
   }
   const uint32_t tmem = tmem_base, tS = 0, tO = 128;
+  const bool two = L::TWO && wk.len - wk.first_key(p) <= FEW;  // P in two terms
 
   if (warp == 0) {
     // ------------------------------------------------------------------ TMA producer: lane x loads
@@ -471,7 +478,7 @@ __global__ void __launch_bounds__(NT, 2) paged_attn_kernel(const __grid_constant
         // P is in shared memory (and the accumulator of the tile before it has been read)
         if (!wait_bar(&p_ready, jp & 1, limit, &abort_flag, p.st, 714)) return false;
         tc_fence_after();
-        const uint32_t pb = (jp & 1) * L::P_BYTES;
+        const uint32_t pb = L::NB == 2 ? (jp & 1) * L::PB : 0;
         if constexpr (F8) {
           constexpr uint32_t ID = idesc_f8(MH, D, 0, 1, 0);
           const uint64_t va = sdesc(smem_u32(sR + s * SLOT), TILE * 128, 1024);
@@ -484,8 +491,12 @@ __global__ void __launch_bounds__(NT, 2) paged_attn_kernel(const __grid_constant
           constexpr uint32_t ID = idesc_bf16(MH, D, 0, 1);
           const uint64_t va = sdesc(smem_u32(sR + s * SLOT), TILE * 128, 1024);
 #pragma unroll
-          for (int kk = 0; kk < TILE / 16; ++kk)
-            umma_ss(tmem + tO, sdesc_at(pa, pb + (kk / 4) * (MH * 128) + (kk % 4) * 32), sdesc_at(va, kk * 2048), ID, kk > 0);
+          for (int h = 0; h < (L::TWO ? 2 : 1); ++h)
+            if (h == 0 || two)
+#pragma unroll
+            for (int kk = 0; kk < TILE / 16; ++kk)
+              umma_ss(tmem + tO, sdesc_at(pa, pb + h * L::P_BYTES + (kk / 4) * (MH * 128) + (kk % 4) * 32),
+                      sdesc_at(va, kk * 2048), ID, h + kk > 0);
         }
         umma_commit(&o_full);
         umma_commit(&r_empty[s]);
@@ -638,39 +649,59 @@ __global__ void __launch_bounds__(NT, 2) paged_attn_kernel(const __grid_constant
         const float neg = mt == -INFINITY ? 0.f : F8 ? 8.f - mt : -mt;
         float la = 0.f, lb = 0.f;
         // P -> shared memory, K-major, 16 bytes of codes as soon as they are there
-        const uint32_t pb = smem_u32(sP) + ((js - 1) & 1) * L::P_BYTES;
-        constexpr int CK = F8 ? 16 : 8;  // keys of a chunk
+        const uint32_t pb = smem_u32(sP) + (L::NB == 2 ? ((js - 1) & 1) * L::PB : 0);
+        if (L::NB == 1 && i > 0 && !add_o()) { ok = false; break; }  // (the last product reads it)
+        auto probabilities = [&](auto two_) {
+          constexpr bool TT = decltype(two_)::value;
+          constexpr int CK = F8 ? 16 : 8;  // keys of a chunk
 #pragma unroll
-        for (int k0 = 0; k0 < SC; k0 += CK) {
-          uint32_t pk[CK / 2];  // bf16 pairs; e4m3: the hi codes of four keys, then the lo codes
+          for (int k0 = 0; k0 < SC; k0 += CK) {
+            uint32_t pk[TT ? CK : CK / 2];  // bf16 pairs, their rests; e4m3: hi codes of four keys, then lo codes
 #pragma unroll
-          for (int k = 0; k < CK; k += 4) {
-            float e[4];
-            const float* v = sv + k0 + k;
-            ffma2(e[0], e[1], v[0], v[1], c, c, neg, neg);
-            ffma2(e[2], e[3], v[2], v[3], c, c, neg, neg);
+            for (int k = 0; k < CK; k += 4) {
+              float e[4];
+              const float* v = sv + k0 + k;
+              ffma2(e[0], e[1], v[0], v[1], c, c, neg, neg);
+              ffma2(e[2], e[3], v[2], v[3], c, c, neg, neg);
 #pragma unroll
-            for (int y = 0; y < 4; ++y) e[y] = fast_exp2(e[y]);
-            fadd2(la, lb, la, lb, e[0], e[1]);
-            fadd2(la, lb, la, lb, e[2], e[3]);
-            if constexpr (F8) {
-              uint32_t h0, l0, h1, l1;
-              split_e4m3(pack_f16x2(e[0], e[1]), h0, l0);
-              split_e4m3(pack_f16x2(e[2], e[3]), h1, l1);
-              pk[k / 4] = h0 | (h1 << 16);
-              pk[CK / 4 + k / 4] = l0 | (l1 << 16);
-            } else {
-              pk[k / 2] = pack_bf16x2(e[0], e[1]);
-              pk[k / 2 + 1] = pack_bf16x2(e[2], e[3]);
+              for (int y = 0; y < 4; ++y) e[y] = fast_exp2(e[y]);
+              fadd2(la, lb, la, lb, e[0], e[1]);
+              fadd2(la, lb, la, lb, e[2], e[3]);
+              if constexpr (F8) {
+                uint32_t h0, l0, h1, l1;
+                split_e4m3(pack_f16x2(e[0], e[1]), h0, l0);
+                split_e4m3(pack_f16x2(e[2], e[3]), h1, l1);
+                pk[k / 4] = h0 | (h1 << 16);
+                pk[CK / 4 + k / 4] = l0 | (l1 << 16);
+              } else {
+#pragma unroll
+                for (int y = 0; y < 2; ++y) {
+                  if constexpr (TT) {
+                    // the first term cut off, not rounded: the rest is positive, and no zero (2^-126 at least), so that
+                    // its product with an infinite value is that infinity again
+                    const uint32_t h0 = __float_as_uint(e[2 * y]) & 0xFFFF0000u;
+                    const uint32_t h1 = __float_as_uint(e[2 * y + 1]) & 0xFFFF0000u;
+                    pk[k / 2 + y] = (h0 >> 16) | h1;
+                    uint32_t r = pack_bf16x2(e[2 * y] - __uint_as_float(h0), e[2 * y + 1] - __uint_as_float(h1));
+                    asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(r) : "r"(0x00800080u));
+                    pk[CK / 2 + k / 2 + y] = r;
+                  } else {
+                    pk[k / 2 + y] = pack_bf16x2(e[2 * y], e[2 * y + 1]);
+                  }
+                }
+              }
             }
+            const int ch = (s0 + k0) / CK;
+            const uint32_t dst = pb + (ch / 8) * (MH * 128) + sw128_off(row, ch % 8);
+            st_shared_v4(dst, pk[0], pk[1], pk[2], pk[3]);
+            if constexpr (F8) st_shared_v4(dst + MH * 128, pk[4], pk[5], pk[6], pk[7]);
+            if constexpr (TT) st_shared_v4(dst + L::P_BYTES, pk[4], pk[5], pk[6], pk[7]);
           }
-          const int ch = (s0 + k0) / CK;
-          const uint32_t dst = pb + (ch / 8) * (MH * 128) + sw128_off(row, ch % 8);
-          st_shared_v4(dst, pk[0], pk[1], pk[2], pk[3]);
-          if constexpr (F8) st_shared_v4(dst + MH * 128, pk[4], pk[5], pk[6], pk[7]);
-        }
+        };
+        if (two) probabilities(std::integral_constant<bool, L::TWO>{});
+        else probabilities(std::false_type{});
         // the last tile's product before this tile's may overwrite it
-        if (i > 0 && !add_o()) { ok = false; break; }
+        if (L::NB == 2 && i > 0 && !add_o()) { ok = false; break; }
         // factors of this tile's product
         const float mn = fmaxf(m_run, mt);
         al = m_run == mn ? 1.f : m_run == -INFINITY ? 0.f : fast_exp2(m_run - mn);
@@ -925,7 +956,7 @@ static int gcd(int a, int b) { return b == 0 ? a : gcd(b, a % b); }
 
 template <int D, bool F8>
 static cudaError_t launch(const CUtensorMap& tk, const CUtensorMap& tv, const Params& p, cudaStream_t st) {
-  using L = Lay<D, F8>;
+  using L = Lay<D, F8, false>;
   const auto k = paged_attn_kernel<D, F8, false>;
   cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, L::BYTES);
   if (e != cudaSuccess) return e;
@@ -939,7 +970,7 @@ static cudaError_t launch(const CUtensorMap& tk, const CUtensorMap& tv, const Pa
 }
 template <int D, bool F8>
 static cudaError_t launch_clusters(const CUtensorMap& tk, const CUtensorMap& tv, const Params& p, cudaStream_t st) {
-  using L = Lay<D, F8>;
+  using L = Lay<D, F8, true>;
   const auto k = paged_attn_kernel<D, F8, true>;
   cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, L::BYTES);
   if (e != cudaSuccess) return e;
