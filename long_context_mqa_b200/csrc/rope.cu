@@ -434,7 +434,7 @@ __global__ void __launch_bounds__(1024) rope_dw_kernel(const float* part, int n,
   griddep_launch_dependents();
   const int c = blockIdx.x * 32 + (threadIdx.x & 31), strip = threadIdx.x >> 5;
   float a = 0.f;
-  constexpr int U = 10;  // records in flight: two rounds of reads for the 592 there are at most on 148 SMs
+  constexpr int U = 19;  // records in flight: one round of reads for the 592 there are at most on 148 SMs
   for (int i = strip; i < n; i += 32 * U) {
     float v[U];
 #pragma unroll

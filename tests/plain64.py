@@ -88,10 +88,10 @@ def cached(pages, table_row, at, e4m3=False, scale=1.0):
     return rows.view(torch.float8_e4m3fn).double() * scale if e4m3 else rows.double()
 
 
-def paged_attn(q, k_pages, v_pages, table, lens, scale, window=0, ks=None, vs=None):
+def paged_attn(q, k_pages, v_pages, table, lens, scale, window=0, ks=None, vs=None, p_round=BF16):
     """(out, lse, bound_out, bound_lse) with pools [n_pages, page, Hk, d].
 
-    Bounds. Every probability is rounded once: to bf16, or to two e4m3 terms (2^-4 times 2^-4 of the value, and
+    Bounds. Every probability is rounded once: to bf16 (p_round), or to two e4m3 terms (2^-4 times 2^-4 of the value, and
     half a step of the second term, 2^-10, where the tile's largest probability counts 256: 2^-18 of it; a
     tile is 128 keys), then the output once more. A score is a sum of d products in 32 bits: 2^-16 of their
     absolute sum; an e4m3 cache's query elements are off by 2^-20 of the head's largest at most. 2^-13 for
@@ -116,7 +116,7 @@ def paged_attn(q, k_pages, v_pages, table, lens, scale, window=0, ks=None, vs=No
         ds = 2.0 ** -16 * torch.einsum("hgd,nhd->hgn", qb.abs(), K.abs()).amax(-1) * scale
         if f8:
             ds = ds + 2.0 ** -20 * qb.abs().amax(-1) * K.abs().sum(-1).amax(0)[:, None] * scale
-        e = BF16 * o.abs() + (BF16 + 2.0 ** -13 + 2 * ds[..., None]) * A
+        e = BF16 * o.abs() + (p_round + 2.0 ** -13 + 2 * ds[..., None]) * A
         e = e + 2.0 ** -126 * (1 + V.abs().sum(0)[:, None])
         if f8:
             tile = torch.div(at, 128, rounding_mode="floor") - first // 128

@@ -139,6 +139,21 @@ def test_infinities_and_nan(hs2):
     assert bool(torch.isfinite(out[0, 0, :, :7]).all()) and bool(torch.isfinite(out[0, 0, :, 8:]).all())
 
 
+@pytest.mark.parametrize("Hq,Hk,d,page", [(1, 1, 128, 16), (3, 3, 64, 48), (64, 1, 128, 128), (16, 2, 64, 16)])
+def test_few_keys_keep_their_weights(hs2, Hq, Hk, d, page):
+    """Short sequences and windows hold probabilities in two bf16 terms: one cut off (2^-7), the rest rounded by half a
+    step of its own (2^-8 of it), 2^-15 together."""
+    c = Cache([2, 3, 7, 64, 65, 256, 1], Hq, Hk, d, page)
+    for window in (0, 2, 5):
+        out, lse = c.run(hs2, window=window)
+        want = P.paged_attn(c.q, c.k, c.v, c.table, c.lens, 1 / math.sqrt(d), window, p_round=2.0 ** -15)
+        near(out, want[0], want[2], "out")
+    c = Cache([2000, 900], Hq, Hk, d, page)  # (few of many keys are visible)
+    out, _ = c.run(hs2, window=130)
+    want = P.paged_attn(c.q, c.k, c.v, c.table, c.lens, 1 / math.sqrt(d), 130, p_round=2.0 ** -15)
+    near(out, want[0], want[2], "out")
+
+
 @pytest.mark.parametrize("f8", [False, True])
 def test_query_magnitudes(hs2, f8):
     """Query rows of zeros, of tiny, of large and of one large element among tiny ones."""
