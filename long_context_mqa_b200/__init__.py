@@ -779,9 +779,10 @@ def qk_norm_rope_bwd(q, k, positions, inv_freq, dq_out, dk_out, *, q_weight=None
                                     eps=eps, interleaved=interleaved, mscale=mscale, dq=dq, dk=dk, dq_weight=dq_weight,
                                     dk_weight=dk_weight, workspace=workspace)
     m = _marshal()
-    new = lambda t: torch.empty(t.shape, dtype=torch.bfloat16, device=t.device)
-    dq = new(q) if dq is None else dq
-    dk = new(k) if dk is None and k is not None else dk
+    if dq is None:
+        dq = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+    if dk is None and k is not None:
+        dk = torch.empty(k.shape, dtype=torch.bfloat16, device=k.device)
     if q_weight is not None and dq_weight is None:
         dq_weight = torch.empty(q.shape[-1], dtype=torch.float32, device=q.device)
     if k_weight is not None and dk_weight is None:
@@ -790,14 +791,14 @@ def qk_norm_rope_bwd(q, k, positions, inv_freq, dq_out, dk_out, *, q_weight=None
     kept = workspace is None
     if kept:
         workspace = _stream_workspace(q, "rope_bwd", st)
-    call = lambda ws: m.qk_norm_rope_bwd(q, k, positions, inv_freq, dq_out, dk_out, q_weight, k_weight, eps, interleaved,
-                                         mscale, dq, dk, dq_weight, dk_weight, ws, kept, st)
-    code = call(workspace)
+    code = m.qk_norm_rope_bwd(q, k, positions, inv_freq, dq_out, dk_out, q_weight, k_weight, eps, interleaved, mscale, dq,
+                              dk, dq_weight, dk_weight, workspace, kept, st)
     if code == ERR_WORKSPACE and kept:  # (the first call of this size)
         heads = 0 if k is None else k.shape[-2] if k.dim() == q.dim() else 1
         with torch.cuda.device(q.device):  # (the size goes by the device's number of SMs)
             nbytes = qk_norm_rope_bwd_workspace_bytes(q.shape[:-2].numel(), q.shape[-2], heads, q.shape[-1])
-        code = call(_stream_workspace(q, "rope_bwd", st, nbytes))
+        code = m.qk_norm_rope_bwd(q, k, positions, inv_freq, dq_out, dk_out, q_weight, k_weight, eps, interleaved, mscale,
+                                  dq, dk, dq_weight, dk_weight, _stream_workspace(q, "rope_bwd", st, nbytes), kept, st)
     _check(code, "hs2_qk_norm_rope_bwd")
     return dq, dk, dq_weight, dk_weight
 
@@ -892,13 +893,13 @@ def paged_attn(q, k_pages, v_pages, page_table, lens, *, k_scale=None, v_scale=N
     kept = workspace is None
     if kept:
         workspace = _stream_workspace(q, "paged_attn", st)
-    call = lambda ws: m.paged_attn(q, k_pages, v_pages, page_table, lens, f8, ks, vs, scale, window, out, lse, ws, kept, st)
-    code = call(workspace)
+    code = m.paged_attn(q, k_pages, v_pages, page_table, lens, f8, ks, vs, scale, window, out, lse, workspace, kept, st)
     if code == ERR_WORKSPACE and kept:  # (the first call of this size)
         heads = k_pages.shape[2] if k_pages.dim() == 4 else 1
         with torch.cuda.device(q.device):  # (the size goes by the device's number of SMs)
             nbytes = paged_attn_workspace_bytes(q.shape[0], q.shape[-2], heads, q.shape[-1])
-        code = call(_stream_workspace(q, "paged_attn", st, nbytes))
+        code = m.paged_attn(q, k_pages, v_pages, page_table, lens, f8, ks, vs, scale, window, out, lse,
+                            _stream_workspace(q, "paged_attn", st, nbytes), kept, st)
     _check(code, "hs2_paged_attn")
     return out, lse
 
