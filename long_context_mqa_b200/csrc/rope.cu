@@ -22,7 +22,7 @@
 //
 // Measured against a copy's 6.56 TB/s: 32k tokens of 64 + 1 heads of 128, 185 us (5.9 TB/s; 200 us when a
 // long run holds the clocks at the power limit), their gradient 305 us (5.4; 320); 4,099 tokens of 32 + 8 heads
-// into e4m3 pages 21.5 us (4.3): one wave of warps, each waiting for six batches of rows in turn. Tried
+// into e4m3 pages 20 us (4.6): one wave of warps, each waiting for six batches of rows in turn. Tried
 // and slower: rings in shared memory filled by cp.async for the gradient (368 us; it is the sums' chain that
 // waits), more and smaller batches at a higher occupancy (492), L2 prefetch of a warp's rows (211 for the
 // forward), streaming cache hints (no difference).
@@ -261,21 +261,30 @@ __global__ void __launch_bounds__(NT, 8) rope_fwd_kernel(Params p) {
         }
       }
     });
-  if (PAGED && vc >= 0) {  // the values as they are, 8 adjacent elements a lane
+  if (PAGED && vc >= 0) {  // the values as they are, 8 adjacent elements a lane, U passes on their way at once
     const int li8 = (lane % LPR) * 8;
-    for (int i = max(p0, nq + nk); i < p1; ++i) {
-      const int h = (i - nq - nk) * RPW + sub;
-      if (h >= p.Hk) continue;
-      const uint4 w = __ldg(reinterpret_cast<const uint4*>(p.v + t * p.v_ts + h * p.v_hs + li8));
-      const long long at = vc + h * p.vp_hs + li8;
-      if (F8) {
-        V8 x;
-        unpack4(make_uint2(w.x, w.y), x.x);
-        unpack4(make_uint2(w.z, w.w), x.x + 4);
-        scale8(x, x, p.v_inv);
-        *reinterpret_cast<uint2*>((uint8_t*)p.v_pages + at) = make_uint2(pack4_e4m3(x.x), pack4_e4m3(x.x + 4));
-      } else {
-        *reinterpret_cast<uint4*>((__nv_bfloat16*)p.v_pages + at) = w;
+    const __nv_bfloat16* src = p.v + t * p.v_ts + li8;
+    for (int i = max(p0, nq + nk); i < p1; i += U) {
+      uint4 w[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int h = (i + u - nq - nk) * RPW + sub;
+        if (i + u < p1 && h < p.Hk) w[u] = __ldg(reinterpret_cast<const uint4*>(src + h * p.v_hs));
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int h = (i + u - nq - nk) * RPW + sub;
+        if (i + u >= p1 || h >= p.Hk) continue;
+        const long long at = vc + h * p.vp_hs + li8;
+        if (F8) {
+          V8 x;
+          unpack4(make_uint2(w[u].x, w[u].y), x.x);
+          unpack4(make_uint2(w[u].z, w[u].w), x.x + 4);
+          scale8(x, x, p.v_inv);
+          *reinterpret_cast<uint2*>((uint8_t*)p.v_pages + at) = make_uint2(pack4_e4m3(x.x), pack4_e4m3(x.x + 4));
+        } else {
+          *reinterpret_cast<uint4*>((__nv_bfloat16*)p.v_pages + at) = w[u];
+        }
       }
     }
   }
