@@ -28,11 +28,11 @@
 // the order of the ranges, so results do not vary from run to run. Short sequences take clusters instead.
 //
 // Measured against 6.56 TB/s, the memory's rate for a copy, in passes one after the other: 8 sequences of
-// 256k tokens, 64 heads on one key head, 172 us (6.25 TB/s; 184 us when a long run holds the clocks at the
+// 256k tokens, 64 heads on one key head, 171 us (6.3 TB/s; 183 us when a long run holds the clocks at the
 // power limit); 48 of up to 8k, 32 heads on 8 in pages of 16, 95 us (6.2); e4m3 codes, 8 of up to 256k, 70 us
-// (4.6; 85 us at the power limit). There the tensor cores are 60% busy (M = 64 runs at half their rate, and
+// (4.7; 84 us at the power limit). There the tensor cores are 60% busy (M = 64 runs at half their rate, and
 // both operands have two terms), and the softmax warps' chain from scores to P is as long as a tile's
-// load. About 12 us of the long cases are start and end: the first tiles' way, the last tiles' chain, the join.
+// load. About 10 us of the long cases are start and end: the first tiles' way, the last tiles' chain, the join.
 // Tried and slower: eight softmax warps of half the columns with their maxima exchanged (140 us for 118 at
 // 8 x 256k of e4m3); a part of the exponentials on the FMA pipe (114 for 110); the products of a row kept
 // in tensor memory with the row rescaled when its maximum moves (bf16 1% faster at 16k, e4m3 3% slower, or
