@@ -668,7 +668,10 @@ def bridge_kv_proj(h, w, *, out=None, workspace=None, stream=None):
 
 # -------------------------------------------------------------------------------------------------
 # around the paged cache: head norms and rotation, page tables, attention without selection. These
-# calls check their tensors in the C++ marshalling module (built with the library).
+# calls check their tensors in the C++ marshalling module (built with the library). Where a call takes a
+# `workspace` (zero-filled uint8, at least what the *_workspace_bytes query or 256 says), one workspace
+# serves one call at a time: calls on different streams and captured graphs that may run at once need one
+# each. Without one, a call uses the binding's own for its stream.
 # -------------------------------------------------------------------------------------------------
 def _marshal():
     if _fast is None:

@@ -49,7 +49,7 @@ class Pool:
 
 
 @pytest.mark.parametrize("B,page,most,seed", [(1, 16, 40, 0), (3, 1, 9, 1), (33, 128, 3000, 2), (512, 16, 60, 3),
-                                              (513, 48, 200, 4), (4096, 16, 5, 5)])
+                                              (513, 48, 200, 4), (4096, 16, 5, 5), (300, 64, 1500, 6)])
 def test_steps_of_mixed_requests(hs2, B, page, most, seed):
     """Several steps in place: requests grow by nothing, one token and chunks, are cut back, end and begin again."""
     r = random.Random(seed)

@@ -26,7 +26,8 @@ def inputs(T, Hq, Hk, d, rot, norm, seed=1, first=0):
 
 
 SHAPES = [(1, 1, 1, 64, 64, 0), (7, 5, 2, 128, 32, 1000), (33, 64, 1, 128, 128, 1048576), (300, 3, 3, 64, 16, 2 ** 24),
-          (2500, 8, 1, 128, 64, 7), (5, 17, 0, 128, 128, 40)]
+          (2500, 8, 1, 128, 64, 7), (5, 17, 0, 128, 128, 40),
+          (40001, 3, 1, 64, 32, 0), (2, 1024, 9, 64, 48, 9)]
 
 
 @pytest.mark.parametrize("norm", [None, torch.float32, torch.bfloat16])
