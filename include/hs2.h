@@ -423,8 +423,9 @@ HS2_API hs2_status hs2_qk_norm_rope_paged(const hs2_bf16* Q, const hs2_bf16* K, 
  * Recorded as HS2_ERR_DEVICE_BOUNDS, with the call otherwise carried out: a length or an end outside
  * [0, max_pages * page_size] and a request whose pages the free list cannot give (requests are served in
  * order, and none that needs pages overtakes one that could not be served; those that need none always
- * are): such a request keeps its length, its rows get slot -1; more new tokens than max_tokens (the rows
- * past it are not written, nor the table entries that they would begin); more free pages than the ring holds (none is given back).
+ * are), and a request whose rows do not all lie before max_tokens (nor do those of any with new tokens after
+ * it): such a request keeps its length and its pages, and takes none; its rows, as far as they lie before
+ * max_tokens, get their positions and slot -1. More free pages than the ring holds (none is given back).
  * Supported: 1 <= B <= 4096. Workspace: hs2_page_table_update_workspace_bytes (zero-filled before its
  * first use).
  */

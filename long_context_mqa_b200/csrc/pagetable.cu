@@ -5,7 +5,8 @@
 // requests' new pages are taken from its head in request order (an exclusive prefix sum of the pages
 // that each lacks), pages given back are appended behind its tail, and the two ranges never meet
 // because the ring has room for every page of the pool. A granted request's new tokens, packed in
-// request order, get a position each (lens[b], lens[b] + 1, ..) and a slot (page * page_size + row).
+// request order, get a position each (lens[b], lens[b] + 1, ..) and a slot (page * page_size + row). A request that the
+// free pages or the packed rows do not suffice for is left as it was.
 //
 // The work is a prefix sum over at most 4,096 requests and then independent items: one per token row
 // and one per returned page, each finding its request by a binary search in the sums. Every block
@@ -136,8 +137,10 @@ __global__ void __launch_bounds__(NT) page_table_kernel(Params p) {
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
     const int b = tid * PER + i;
-    bool granted = grow[i] >= 0;
-    if (grow[i] > 0) {
+    // its rows have to lie within the packed ones, all of them (a page is entered by the token that is its first);
+    // those of every later request with new tokens lie behind them
+    bool granted = grow[i] >= 0 && (rows[i] == 0 || at[0] + rows[i] <= p.T);
+    if (granted && grow[i] > 0) {
       granted = at[1] <= avail && grow[i] <= avail - at[1];  // in request order, while they last
       if (granted) used = at[1] + grow[i];
       else bad = true;
