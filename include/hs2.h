@@ -425,7 +425,9 @@ HS2_API hs2_status hs2_qk_norm_rope_paged(const hs2_bf16* Q, const hs2_bf16* K, 
  * order, and none that needs pages overtakes one that could not be served; those that need none always
  * are), and a request whose rows do not all lie before max_tokens (nor do those of any with new tokens after
  * it): such a request keeps its length and its pages, and takes none; its rows, as far as they lie before
- * max_tokens, get their positions and slot -1. More free pages than the ring holds (none is given back).
+ * max_tokens, get their positions and slot -1. More free pages than the ring holds with those given back: none
+ * is, and the requests that would have given pages back keep their lengths. A head or count outside the ring:
+ * no page is taken or given back.
  * Supported: 1 <= B <= 4096. Workspace: hs2_page_table_update_workspace_bytes (zero-filled before its
  * first use).
  */

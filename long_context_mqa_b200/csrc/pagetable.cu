@@ -6,7 +6,7 @@
 // that each lacks), pages given back are appended behind its tail, and the two ranges never meet
 // because the ring has room for every page of the pool. A granted request's new tokens, packed in
 // request order, get a position each (lens[b], lens[b] + 1, ..) and a slot (page * page_size + row). A request that the
-// free pages or the packed rows do not suffice for is left as it was.
+// free pages or the packed rows do not suffice for, or whose pages the ring cannot take back, is left as it was.
 //
 // The work is a prefix sum over at most 4,096 requests and then independent items: one per token row
 // and one per returned page, each finding its request by a binary search in the sums. Every block
@@ -133,6 +133,9 @@ __global__ void __launch_bounds__(NT) page_table_kernel(Params p) {
   }
   const int rows_all = all[0], back_all = all[2];
   const int avail = state_ok ? count : 0;
+  // more pages than the ring holds with those given back (the caller's lists disagree): none is
+  const bool room = state_ok && (long long)count + back_all <= p.cap;
+  if (!room && back_all > 0) bad = true;
   int used = 0;
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
@@ -153,7 +156,7 @@ __global__ void __launch_bounds__(NT) page_table_kernel(Params p) {
     at[0] = sat_add(at[0], rows[i]);
     at[1] = sat_add(at[1], max(grow[i], 0));
     at[2] = sat_add(at[2], gone[i]);
-    if (!granted) want_len[i] = len[i];
+    if (!granted || (gone[i] > 0 && !room)) want_len[i] = len[i];
   }
   used = __reduce_max_sync(0xffffffffu, used);
   if (lane == 0 && used > 0) atomicMax(&s_used, used);
@@ -161,9 +164,6 @@ __global__ void __launch_bounds__(NT) page_table_kernel(Params p) {
     tok[p.B] = rows_all;
     back[p.B] = back_all;
   }
-  // more pages than the ring holds with those given back: the caller's lists disagree
-  const bool room = state_ok && (long long)count + back_all <= p.cap;
-  if (!room && back_all > 0) bad = true;
   if (rows_all > p.T) bad = true;
   const bool any_bad = __syncthreads_or(bad);
   if (any_bad && blockIdx.x == 0 && tid == 0) report_status(p.st, kStatusBounds, 601);

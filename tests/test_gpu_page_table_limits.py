@@ -1,5 +1,6 @@
-"""page_table_update where a step does not fit: more new tokens than rows. Every request is either served whole or left
-as it was, and no page is lost or owned twice. Whole numbers, against one request after the other on the host."""
+"""page_table_update where a step does not fit: more new tokens than rows, a ring too small for what comes back.
+Every request is either served whole or left as it was, and no page is lost or owned
+twice. Whole numbers, against one request after the other on the host."""
 import random
 
 import pytest
@@ -130,3 +131,28 @@ def test_many_steps_keep_every_page(hs2, B, page, most, seed):
         some += not p.step(hs2, d, r.choice([total, total + 5, total // 2, max(total - 1, 0)]))
         assert p.owners() == before
     assert some > 2
+
+
+def test_a_ring_too_small_for_what_comes_back(hs2):
+    """Nothing is given back, and the requests that would have given pages keep their lengths; the others are served."""
+    p = Pool(4, 5, 16, 20, [64, 40, 20, 16], cap=6)
+    kept = p.owners()
+    # (the ring of six is full)
+    assert not p.step(hs2, [-64, -33, -2, 0], 0)
+    assert p.lens == [64, 40, 18, 16] and p.owners() == kept
+    assert not p.step(hs2, [-64, 0, 20, 1], 21)
+    assert p.lens == [64, 40, 38, 17] and p.owners() == kept
+    assert p.step(hs2, [0, -33, 0, 0], 0)  # (two fit now)
+    assert p.lens == [64, 7, 38, 17] and p.owners() == kept
+
+
+@pytest.mark.parametrize("state", [[-1, 2], [9, 2], [0, 10], [0, -1]])
+def test_a_state_that_is_none(hs2, state):
+    """A head or count outside the ring: no page is taken or given back, and no length changes that would."""
+    p = Pool(4, 5, 16, 9, [16, 33, 20, 5])
+    t, ring = p.t.clone(), p.r.clone()
+    lo, so, _, _, slots = hs2.page_table_update(p.t, p.l, dev([20, -20, 3, -1]), p.r, dev(state), 16, 23, workspace=p.ws)
+    assert hs2.read_device_status(p.ws) == hs2.ERR_DEVICE_BOUNDS
+    assert lo.tolist() == [16, 33, 23, 4] and so.tolist() == state
+    assert torch.equal(p.t, t) and torch.equal(p.r, ring)
+    assert slots.tolist() == [-1] * 20 + [p.table[2][1] * 16 + 4 + i for i in range(3)]
