@@ -427,7 +427,8 @@ HS2_API hs2_status hs2_qk_norm_rope_paged(const hs2_bf16* Q, const hs2_bf16* K, 
  * it): such a request keeps its length and its pages, and takes none; its rows, as far as they lie before
  * max_tokens, get their positions and slot -1. More free pages than the ring holds with those given back: none
  * is, and the requests that would have given pages back keep their lengths. A head or count outside the ring:
- * no page is taken or given back.
+ * no page is taken or given back. A page id that is none, negative or with a slot past 32 bits: the rows in that
+ * page get slot -1 (the request's length counts them), and one that is given back goes into the ring as it is.
  * Supported: 1 <= B <= 4096. Workspace: hs2_page_table_update_workspace_bytes (zero-filled before its
  * first use).
  */

@@ -188,14 +188,19 @@ __global__ void __launch_bounds__(NT) page_table_kernel(Params p) {
             if (r == 0) p.table[(size_t)b * p.width + j] = pg;
           }
           slot = (long long)pg * p.page + r;
-          if (pg < 0 || slot > 0x7FFFFFFFll) slot = -1;
+          if (pg < 0 || slot > 0x7FFFFFFFll) {  // no page's id
+            slot = -1;
+            report_status(p.st, kStatusBounds, 602);
+          }
         }
       }
       p.pos[it] = pos;
       p.slots[it] = (int)slot;
     } else {
       const int i = it - p.T, b = find(back, p.B, i);
-      p.ring[wrap((unsigned)head + (unsigned)(count + i))] = p.table[(size_t)b * p.width + held_len[b] + i - back[b]];
+      const int pg = p.table[(size_t)b * p.width + held_len[b] + i - back[b]];
+      if (pg < 0 || (long long)pg * p.page > 0x7FFFFFFFll) report_status(p.st, kStatusBounds, 603);
+      p.ring[wrap((unsigned)head + (unsigned)(count + i))] = pg;
     }
   }
   if (blockIdx.x == 0)

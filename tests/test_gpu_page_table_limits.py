@@ -1,5 +1,5 @@
-"""page_table_update where a step does not fit: more new tokens than rows, a ring too small for what comes back.
-Every request is either served whole or left as it was, and no page is lost or owned
+"""page_table_update where a step does not fit: more new tokens than rows, a ring too small for what comes back,
+page ids that are none. Every request is either served whole or left as it was, and no page is lost or owned
 twice. Whole numbers, against one request after the other on the host."""
 import random
 
@@ -156,3 +156,31 @@ def test_a_state_that_is_none(hs2, state):
     assert lo.tolist() == [16, 33, 23, 4] and so.tolist() == state
     assert torch.equal(p.t, t) and torch.equal(p.r, ring)
     assert slots.tolist() == [-1] * 20 + [p.table[2][1] * 16 + 4 + i for i in range(3)]
+
+
+def test_page_ids_that_are_none_are_recorded(hs2):
+    """A negative id, or one whose slot passes 32 bits: in the table under a new token, at the ring's head, and in what is
+    given back."""
+    for bad in (-1, -2 ** 31, 2 ** 31 - 1):
+        for where in ("table", "ring"):
+            p = Pool(2, 4, 16, 8, [10, 16])
+            if where == "table":
+                p.t[0, 0] = bad
+            else:
+                p.r[p.head] = bad
+            _, _, _, pos, slots = hs2.page_table_update(p.t, p.l, dev([3, 2]), p.r, p.s, 16, 5, workspace=p.ws)
+            assert hs2.read_device_status(p.ws) == hs2.ERR_DEVICE_BOUNDS, (bad, where)
+            assert pos.tolist() == [10, 11, 12, 16, 17]
+            good = slots[3:] if where == "table" else slots[:3]
+            none = slots[:3] if where == "table" else slots[3:]
+            assert int(good.min()) >= 0 and bool((none == -1).all())
+    for bad in (-1, -2 ** 31, 2 ** 31 - 1):
+        p = Pool(2, 4, 16, 8, [40, 16])
+        p.t[0, 1] = bad
+        hs2.page_table_update(p.t, p.l, dev([-40, 0]), p.r, p.s, 16, 0, workspace=p.ws)
+        assert hs2.read_device_status(p.ws) == hs2.ERR_DEVICE_BOUNDS, bad
+    # a request that stands still, or one whose tokens lie elsewhere: its other entries are not read
+    p = Pool(2, 4, 16, 8, [40, 16])
+    p.t[0, 0] = -1
+    hs2.page_table_update(p.t, p.l, dev([1, 0]), p.r, p.s, 16, 1, workspace=p.ws)
+    assert hs2.read_device_status(p.ws) == 0
