@@ -389,7 +389,7 @@ HS2_API hs2_status hs2_qk_norm_rope_bwd(const hs2_bf16* Q, const hs2_bf16* K, lo
  * k_pages, v_pages  pools of n_pages pages: element e of head h of row r of page g at [g * strides[0] +
  *      r * strides[1] + h * strides[2] + e] (k_page_strides, v_page_strides: HOST arrays of 3, in
  *      elements, positive multiples of 16 bytes); bf16, or with e4m3 != 0 codes of K / k_scale and
- *      V / v_scale (rounded once to nearest even, saturating at 448)
+ *      V / v_scale (the real quotient rounded once to nearest even, saturating at 448)
  * Workspace: hs2_qk_norm_rope_paged_workspace_bytes (the status block).
  */
 HS2_API size_t hs2_qk_norm_rope_paged_workspace_bytes(void);
