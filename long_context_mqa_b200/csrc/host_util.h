@@ -49,7 +49,7 @@ inline bool cache_scale_ok(float s) { return s > 0.f && s < HUGE_VALF && 1.f / s
 
 // Launches `kernel` on `stream`; with pdl = true the launch may begin while the previous
 // kernel on the stream is still running (the kernel must call griddep_wait() before it reads
-// anything that kernel wrote).
+// anything that kernel wrote, and not by __ldg, whose data may not change from the kernel's start).
 // With cluster > 1 the grid's x dimension is cut into clusters of that many blocks.
 template <typename... KArgs, typename... Args>
 cudaError_t launch_clusters_k(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream, bool pdl,

@@ -162,7 +162,7 @@ __device__ __forceinline__ void split_e5m2(uint32_t x, uint32_t& hi, uint32_t& l
 // A length that the page table cannot hold counts as none.
 template <int TILE>
 __device__ __forceinline__ int seq_tiles(const Params& p, int b, int& len, int& t0, bool* bad = nullptr) {
-  len = __ldg(p.lens + b);
+  len = p.lens[b];
   if (len < 0 || (long long)len > (long long)p.max_pages * p.page) {
     if (bad) *bad = true;
     len = 0;
@@ -389,7 +389,7 @@ __global__ void __launch_bounds__(NT, 2) paged_attn_kernel(const __grid_constant
       auto page_of = [&](int t) -> int {
         const int k0 = t * TILE + lane * p.box;
         if (lane >= n_box || k0 >= wk.len || k0 + p.box <= first) return kNoPage;
-        const int pg = __ldg(row_ids + k0 / p.page);
+        const int pg = row_ids[k0 / p.page];
         return pg == kNoPage ? -1 : pg;
       };
       auto checked = [&](int pg) -> int {
@@ -539,7 +539,7 @@ __global__ void __launch_bounds__(NT, 2) paged_attn_kernel(const __grid_constant
         uint4 w[D / 16];
 #pragma unroll
         for (int i = 0; i < D / 16; ++i)
-          w[i] = row < p.G ? __ldg(reinterpret_cast<const uint4*>(src + o0) + i) : make_uint4(0u, 0u, 0u, 0u);
+          w[i] = row < p.G ? reinterpret_cast<const uint4*>(src + o0)[i] : make_uint4(0u, 0u, 0u, 0u);
         float am = 0.f, nan = 0.f;
 #pragma unroll
         for (int i = 0; i < D / 16; ++i) {
@@ -580,7 +580,7 @@ __global__ void __launch_bounds__(NT, 2) paged_attn_kernel(const __grid_constant
         uint4 w[OC / 8];
 #pragma unroll
         for (int i = 0; i < OC / 8; ++i)
-          w[i] = row < p.G ? __ldg(reinterpret_cast<const uint4*>(src + o0) + i) : make_uint4(0u, 0u, 0u, 0u);
+          w[i] = row < p.G ? reinterpret_cast<const uint4*>(src + o0)[i] : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
         for (int i = 0; i < OC / 8; ++i) {
           const int ch = o0 / 8 + i;

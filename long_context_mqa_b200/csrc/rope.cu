@@ -215,10 +215,10 @@ __global__ void __launch_bounds__(NT, 8) rope_fwd_kernel(Params p) {
   griddep_launch_dependents();
   const int t = (int)(item / p.parts), part = (int)(item % p.parts);
   if (t >= p.T) return;
-  const int pos = __ldg(p.pos + t);
+  const int pos = p.pos[t];
   int slot = 0;
   if (PAGED) {
-    slot = __ldg(p.slots + t);
+    slot = p.slots[t];
     if (slot < 0) return;  // a padding row: nothing of it is read or written
   }
   const Lane<D, INTER> own(lane, p.rot);
@@ -249,8 +249,8 @@ __global__ void __launch_bounds__(NT, 8) rope_fwd_kernel(Params p) {
         const int h = (i + u) * RPW + sub;
         xa[u] = xb[u] = make_uint2(0u, 0u);
         if (i + u < i1 && h < H) {
-          xa[u] = __ldg(reinterpret_cast<const uint2*>(src + h * hs + own.a));
-          xb[u] = __ldg(reinterpret_cast<const uint2*>(src + h * hs + own.b));
+          xa[u] = *reinterpret_cast<const uint2*>(src + h * hs + own.a);
+          xb[u] = *reinterpret_cast<const uint2*>(src + h * hs + own.b);
         }
       }
       if (i == i0) {
@@ -308,7 +308,7 @@ __global__ void __launch_bounds__(NT, 8) rope_fwd_kernel(Params p) {
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const int h = (i + u - nq - nk) * RPW + sub;
-        if (i + u < p1 && h < p.Hk) w[u] = __ldg(reinterpret_cast<const uint4*>(src + h * p.v_hs));
+        if (i + u < p1 && h < p.Hk) w[u] = *reinterpret_cast<const uint4*>(src + h * p.v_hs);
       }
 #pragma unroll
       for (int u = 0; u < U; ++u) {
@@ -373,20 +373,20 @@ __global__ void __launch_bounds__(NT, 4) rope_bwd_kernel(Params p) {
       for (int u = 0; u < N; ++u) {
         va[u] = vb[u] = ha[u] = hb[u] = make_uint2(0u, 0u);
         if (w && on) {
-          va[u] = __ldg(reinterpret_cast<const uint2*>(xa));
-          vb[u] = __ldg(reinterpret_cast<const uint2*>(xb));
+          va[u] = *reinterpret_cast<const uint2*>(xa);
+          vb[u] = *reinterpret_cast<const uint2*>(xb);
         }
         xa += step;
         xb += step;
         if constexpr (G32) {
           const float4 z = make_float4(0.f, 0.f, 0.f, 0.f);
-          const float4 q0 = on ? __ldg(reinterpret_cast<const float4*>(ga + u * (RPW * D * GB))) : z;
-          const float4 q1 = on ? __ldg(reinterpret_cast<const float4*>(gb + u * (RPW * D * GB))) : z;
+          const float4 q0 = on ? *reinterpret_cast<const float4*>(ga + u * (RPW * D * GB)) : z;
+          const float4 q1 = on ? *reinterpret_cast<const float4*>(gb + u * (RPW * D * GB)) : z;
           gv[u].x[0] = q0.x; gv[u].x[1] = q0.y; gv[u].x[2] = q0.z; gv[u].x[3] = q0.w;
           gv[u].x[4] = q1.x; gv[u].x[5] = q1.y; gv[u].x[6] = q1.z; gv[u].x[7] = q1.w;
         } else if (on) {
-          ha[u] = __ldg(reinterpret_cast<const uint2*>(ga + u * (RPW * D * GB)));
-          hb[u] = __ldg(reinterpret_cast<const uint2*>(gb + u * (RPW * D * GB)));
+          ha[u] = *reinterpret_cast<const uint2*>(ga + u * (RPW * D * GB));
+          hb[u] = *reinterpret_cast<const uint2*>(gb + u * (RPW * D * GB));
         }
       }
       if (!fresh) {
@@ -439,7 +439,7 @@ __global__ void __launch_bounds__(NT, 4) rope_bwd_kernel(Params p) {
     t = (int)(item / p.parts);
     const int p0 = part * per, p1 = min(n_pass, p0 + per);
     if (p0 >= p1) continue;
-    pos = __ldg(p.pos + t);
+    pos = p.pos[t];
     fresh = false;
     if (p0 < nq)
       rows(p0, min(p1, nq), p.Hq, p.q + t * p.q_ts, p.q_hs, p.qw, p.dq_out + (long long)t * p.Hq * D, std::false_type{},
