@@ -29,6 +29,8 @@
 // warps 2..9 the row (or key) threads: a TMEM lane (row or key) is owned by one warp of each of
 // the two warpgroups, which split its 128 columns (warpgroup g takes columns 64 g .. 64 g + 63).
 // Every wait is bounded and reports a timeout.
+#include <type_traits>
+
 #include "decode.h"
 #include "host_util.h"
 #include "pair_union.cuh"
@@ -81,13 +83,21 @@ __global__ void __launch_bounds__(256) bwd_prep_kernel(const __nv_bfloat16* dO, 
                                                        const float* lse, float* Dv, float* lse2, long long n_rows) {
   griddep_wait();
   griddep_launch_dependents();
+  using Word = std::conditional_t<D == 128, uint2, uint32_t>;  // a lane's elements of a row
   const int lane = threadIdx.x & 31;
   const long long nw = (long long)gridDim.x * (blockDim.x / 32);
-  for (long long r = blockIdx.x * (long long)(blockDim.x / 32) + threadIdx.x / 32; r < n_rows; r += nw) {
+  long long r = blockIdx.x * (long long)(blockDim.x / 32) + threadIdx.x / 32;
+  Word a{}, b{};
+  auto load = [&](long long row) {
+    if (row < n_rows) {
+      a = reinterpret_cast<const Word*>(dO + row * D)[lane];
+      b = reinterpret_cast<const Word*>(out + row * D)[lane];
+    }
+  };
+  load(r);
+  for (; r < n_rows; r += nw) {
     float acc = 0.f;
     if constexpr (D == 128) {
-      const uint2 a = __ldg(reinterpret_cast<const uint2*>(dO + r * D) + lane);
-      const uint2 b = __ldg(reinterpret_cast<const uint2*>(out + r * D) + lane);
       const uint32_t aw[2] = {a.x, a.y}, bw[2] = {b.x, b.y};
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
@@ -95,11 +105,10 @@ __global__ void __launch_bounds__(256) bwd_prep_kernel(const __nv_bfloat16* dO, 
         acc += __uint_as_float(aw[x] & 0xFFFF0000u) * __uint_as_float(bw[x] & 0xFFFF0000u);
       }
     } else {
-      const uint32_t a = __ldg(reinterpret_cast<const uint32_t*>(dO + r * D) + lane);
-      const uint32_t b = __ldg(reinterpret_cast<const uint32_t*>(out + r * D) + lane);
       acc = __uint_as_float(a << 16) * __uint_as_float(b << 16) +
             __uint_as_float(a & 0xFFFF0000u) * __uint_as_float(b & 0xFFFF0000u);
     }
+    load(r + nw);  // the next row's are on their way meanwhile
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, o);
     if (lane == 0) {
@@ -276,8 +285,8 @@ __global__ void __launch_bounds__(NT, 1)
       const bool valid = rloc < p.rows_per_batch;
       const int t = p.off + (valid ? rloc / H : 0);
       const long long grow = (long long)b * p.rows_per_batch + rloc;
-      const float nl2 = valid ? -__ldg(p.lse2 + grow) : 0.f;
-      const float Dr = valid ? __ldg(p.Dv + grow) : 0.f;
+      const float nl2 = valid ? -p.lse2[grow] : 0.f;
+      const float Dr = valid ? p.Dv[grow] : 0.f;
       for (int j = 0; j <= jt; ++j) {
         if (!warp_wait(&s_full, ns & 1, limit, &abort_flag, p.st, 721)) { ok = false; break; }
         ++ns;
@@ -676,8 +685,8 @@ __global__ void __launch_bounds__(128, 1) sparse_bwd_kernel(BwdParams p) {
       }
     }
     if (tid < MH) {
-      s_nl2[tid] = tid < H ? -__ldg(p.lse2 + (size_t)r * H + tid) : 0.f;
-      s_D[tid] = tid < H ? __ldg(p.Dv + (size_t)r * H + tid) : 0.f;
+      s_nl2[tid] = tid < H ? -p.lse2[(size_t)r * H + tid] : 0.f;
+      s_D[tid] = tid < H ? p.Dv[(size_t)r * H + tid] : 0.f;
     }
     // gathers the selected K and V rows of tile t into stage t & 1 (16 lanes per 256-byte row,
     // the row's index passed by shuffle from the lane that read it); returns this thread's key
@@ -935,8 +944,8 @@ __global__ void __launch_bounds__(128, 1) sparse_bwd_pair_kernel(BwdParams p) {
       const int m = tid;  // 128 rows, one per thread
       const bool have = m < H || two;
       const size_t g = (size_t)(m < H ? r0 : r1) * H + (m & (H - 1));
-      s_nl2[m] = have ? -__ldg(p.lse2 + g) : 0.f;
-      s_D[m] = have ? __ldg(p.Dv + g) : 0.f;
+      s_nl2[m] = have ? -p.lse2[g] : 0.f;
+      s_D[m] = have ? p.Dv[g] : 0.f;
     }
     // ---- the union of the two rows' selections. Lists that are strictly ascending with any -1
     // slots at the tail (the full layer's output) are merged without duplicates (a key in both

@@ -113,7 +113,7 @@ struct PageRun {
   const int32_t* row;
   int lt, step, left, v0, v1, v2, v3;
   __device__ __forceinline__ int load(int k) const {
-    return row && k < left ? __ldg(row + lt + k * step) : -1;
+    return row && k < left ? row[lt + k * step] : -1;
   }
   __device__ __forceinline__ void start(const int32_t* ptab, int max_pages, int b, int lt0, int st, int n) {
     row = ptab ? ptab + (size_t)b * max_pages : nullptr;

@@ -360,7 +360,7 @@ __global__ void widen_e4m3_kernel(const uint8_t* x, float scale, __nv_bfloat16* 
   griddep_wait();
   const long long stride = (long long)gridDim.x * blockDim.x;
   for (long long i = blockIdx.x * (long long)blockDim.x + threadIdx.x; i < n16; i += stride) {
-    const uint4 w = __ldg(reinterpret_cast<const uint4*>(x) + i);
+    const uint4 w = reinterpret_cast<const uint4*>(x)[i];
     const uint32_t in[4] = {w.x, w.y, w.z, w.w};
     uint32_t o[8];
 #pragma unroll

@@ -62,8 +62,8 @@ __device__ __forceinline__ int pair_union(const int32_t* idx, int S, int Lk, int
 #pragma unroll
     for (int k = 0; k < PER; ++k) {
       const int i = tid + k * UNION_NT;
-      ra[k] = i < S ? __ldg(idx + (size_t)r0 * S + i) : -1;
-      rb[k] = i < nBl ? __ldg(idx + (size_t)(r0 + 1) * S + i) : -1;
+      ra[k] = i < S ? idx[(size_t)r0 * S + i] : -1;
+      rb[k] = i < nBl ? idx[(size_t)(r0 + 1) * S + i] : -1;
     }
 #pragma unroll
     for (int k = 0; k < PER; ++k) {

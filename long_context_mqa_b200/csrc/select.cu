@@ -163,7 +163,7 @@ __global__ void __launch_bounds__(128) sel_rescore_kernel(SelParams p) {
     long long krow = -1;
     if (valid) {
       if (p.ptab) {
-        const int pg = __ldg(p.ptab + (size_t)b * p.max_pages + (j >> 7));
+        const int pg = p.ptab[(size_t)b * p.max_pages + (j >> 7)];
         if (pg >= 0 && pg < p.n_pages) krow = (long long)pg * 128 + (j & 127);
         else { valid = false; report_status(p.st, kStatusBounds, 313); }
       } else {
@@ -177,7 +177,7 @@ __global__ void __launch_bounds__(128) sel_rescore_kernel(SelParams p) {
 #pragma unroll
       for (int it = 0; it < 8; ++it) {
         const long long kr = __shfl_sync(0xffffffffu, krow, 4 * it + sub);
-        x[it] = kr >= 0 ? __ldg(reinterpret_cast<const uint4*>(p.kc8 + (size_t)kr * D) + ch) : make_uint4(0u, 0u, 0u, 0u);
+        x[it] = kr >= 0 ? reinterpret_cast<const uint4*>(p.kc8 + (size_t)kr * D)[ch] : make_uint4(0u, 0u, 0u, 0u);
       }
 #pragma unroll
       for (int it = 0; it < 8; ++it) {

@@ -117,7 +117,7 @@ __global__ void __launch_bounds__(NT, 2) sparse_attn_kernel(SpParams p) {
     long long krow = -1;
     if (valid) {
       if (p.ptab) {
-        const int pg = __ldg(p.ptab + (size_t)b * p.max_pages + (j >> 7));
+        const int pg = p.ptab[(size_t)b * p.max_pages + (j >> 7)];
         valid = pg >= 0 && pg < p.n_pages;
         krow = valid ? (long long)pg * 128 + (j & 127) : -1;
       } else {
@@ -140,8 +140,8 @@ __global__ void __launch_bounds__(NT, 2) sparse_attn_kernel(SpParams p) {
       for (int it = 0; it < 32 / RPS8; ++it) {
         const long long kr = __shfl_sync(0xffffffffu, krow, it * RPS8 + sub8);
         const uint4 z = make_uint4(0u, 0u, 0u, 0u);
-        xk[it] = kr >= 0 ? __ldg(reinterpret_cast<const uint4*>(K8b + (size_t)kr * D) + ch8) : z;
-        xv[it] = kr >= 0 ? __ldg(reinterpret_cast<const uint4*>(V8b + (size_t)kr * D) + ch8) : z;
+        xk[it] = kr >= 0 ? reinterpret_cast<const uint4*>(K8b + (size_t)kr * D)[ch8] : z;
+        xv[it] = kr >= 0 ? reinterpret_cast<const uint4*>(V8b + (size_t)kr * D)[ch8] : z;
       }
       auto put = [&](uint32_t base, int rr, const uint4& x) {
         const uint32_t o = base + (ch8 / 4) * (TILE * 128);

@@ -1,6 +1,7 @@
 """Kernels that are launched while the one before them still runs wait for it and then read what it wrote. A read-only
 load (`__ldg`) asks for data that does not change while the kernel lives, and that wait comes after the
 kernel's start: only numbers that no kernel of the library writes may be read with it (CPU only: the sources)."""
+import glob
 import os
 import re
 
@@ -24,4 +25,9 @@ def read_only_loads(name):
 
 @pytest.mark.parametrize("name", ["rope.cu", "paged_attn.cu", "pagetable.cu"])
 def test_the_operators_around_the_cache_read_no_predecessors_data_as_constant(name):
+    assert read_only_loads(name) == []
+
+
+@pytest.mark.parametrize("name", sorted(os.path.basename(p) for p in glob.glob(os.path.join(CSRC, "*.cu*"))))
+def test_nor_does_what_reads_the_tables_and_pages_that_they_write(name):
     assert read_only_loads(name) == []
