@@ -922,7 +922,7 @@ def cached_workspace(key: str, device=None, stream=None):
     `stream` (the current one)."""
     device = torch.device("cuda", torch.cuda.current_device()) if device is None else device
     ws = _ws_cache.get((device, key))
-    if ws is None:
+    if ws is None and any(len(k) == 3 and k[1] == key for k in list(_ws_cache)):
         stream = torch.cuda.current_stream(device) if stream is None else stream
         ws = _ws_cache.get((stream.device_index, key, stream.cuda_stream))
     return ws
