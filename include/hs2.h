@@ -369,7 +369,8 @@ HS2_API hs2_status hs2_qk_norm_rope(const hs2_bf16* Q, const hs2_bf16* K, long l
  * dq_out [T, Hq, d] bf16, dk_out [T, Hk, d] bf16, or fp32 with dk_out_fp32 != 0 (what the attention's
  *      backward accumulates): contiguous
  * dQ, dK [T, H, d] bf16, contiguous (written); dq_weight, dk_weight [d] fp32 (written; only with weights)
- * The weights' gradients are summed in a fixed order (they do not vary from run to run).
+ * The weights' gradients are summed in a fixed order (they do not vary from run to run). The workspace holds their
+ * parts: without weights none is used (workspace may be NULL).
  */
 HS2_API size_t hs2_qk_norm_rope_bwd_workspace_bytes(int T, int Hq, int Hk, int d);
 HS2_API hs2_status hs2_qk_norm_rope_bwd(const hs2_bf16* Q, const hs2_bf16* K, long long q_token_stride,

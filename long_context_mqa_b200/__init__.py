@@ -791,7 +791,7 @@ def qk_norm_rope_bwd(q, k, positions, inv_freq, dq_out, dk_out, *, q_weight=None
     if k_weight is not None and dk_weight is None:
         dk_weight = torch.empty(q.shape[-1], dtype=torch.float32, device=q.device)
     st = _stream_of(q)
-    kept = workspace is None
+    kept = workspace is None and q_weight is not None  # (without weights there is no scratch)
     if kept:
         workspace = _stream_workspace(q, "rope_bwd", st)
     code = m.qk_norm_rope_bwd(q, k, positions, inv_freq, dq_out, dk_out, q_weight, k_weight, eps, interleaved, mscale, dq,

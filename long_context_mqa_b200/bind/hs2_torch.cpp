@@ -239,7 +239,7 @@ int64_t qk_norm_rope(const at::Tensor& q, const OptT& k, const at::Tensor& posit
 int64_t qk_norm_rope_bwd(const at::Tensor& q, const OptT& k, const at::Tensor& positions, const at::Tensor& inv_freq,
                          const at::Tensor& dq_out, const OptT& dk_out, const OptT& qw, const OptT& kw, double eps,
                          bool interleaved, double mscale, const at::Tensor& dq, const OptT& dk, const OptT& dqw,
-                         const OptT& dkw, const at::Tensor& ws, bool kept, int64_t stream) {
+                         const OptT& dkw, const OptT& ws, bool kept, int64_t stream) {
   const RopeArgs a = rope_args(q, k, positions, inv_freq, qw, kw);
   const void* gq = out_of(dq_out, "dq_out", at::kBFloat16, q);
   void* xq = out_of(dq, "dq", at::kBFloat16, q);
@@ -262,12 +262,13 @@ int64_t qk_norm_rope_bwd(const at::Tensor& q, const OptT& k, const at::Tensor& p
     need_on(*dkw, "dk_weight", at::kFloat, 1, q);
     HS2_ARG_CHECK(dkw->size(0) == a.d, "dk_weight must have ", a.d, " elements");
   }
-  need_ws(ws, q, kept, stream);
+  if (ws.has_value()) need_ws(*ws, q, kept, stream);
   c10::DeviceGuard guard(q.device());
   return g_rope_bwd(a.q.p, a.k.p, a.q.ts, a.q.hs, a.k.ts, a.k.hs, a.pos, a.freq, a.T, a.Hq, a.Hk, a.d, a.rot, interleaved,
                     (float)mscale, (float)eps, a.qw, a.kw, a.f32, gq, gk, g32, xq, xk,
                     dqw.has_value() ? dqw->data_ptr<float>() : nullptr, dkw.has_value() ? dkw->data_ptr<float>() : nullptr,
-                    ws.data_ptr(), (size_t)ws.nbytes(), reinterpret_cast<void*>(stream));
+                    ws.has_value() ? ws->data_ptr() : nullptr, ws.has_value() ? (size_t)ws->nbytes() : 0,
+                    reinterpret_cast<void*>(stream));
 }
 
 // A page pool [n_pages, page, Hk, d] (or [n_pages, page, d]: one head), any strides but the last

@@ -672,7 +672,7 @@ hs2_status hs2_qk_norm_rope_bwd(const hs2_bf16* Q, const hs2_bf16* K, long long 
     return HS2_ERR_INVALID_ARG;
   if (q_weight && (!dq_weight || (Hk > 0 && !dk_weight))) return HS2_ERR_INVALID_ARG;
   if (!rope::shape_ok(d, rot) || !device_is_sm100()) return HS2_ERR_UNSUPPORTED_SHAPE;
-  if (!workspace || !aligned16(workspace) || workspace_bytes < hs2_qk_norm_rope_bwd_workspace_bytes(T, Hq, Hk, d))
+  if (q_weight && (!workspace || !aligned16(workspace) || workspace_bytes < hs2_qk_norm_rope_bwd_workspace_bytes(T, Hq, Hk, d)))
     return HS2_ERR_WORKSPACE;
   const cudaStream_t st = (cudaStream_t)stream;
   rope::Params p{};
@@ -684,7 +684,7 @@ hs2_status hs2_qk_norm_rope_bwd(const hs2_bf16* Q, const hs2_bf16* K, long long 
   p.eps = eps; p.mscale = mscale;
   p.dq_out = (const __nv_bfloat16*)dq_out; p.dk_out = dk_out;
   p.dq = (__nv_bfloat16*)dQ; p.dk = (__nv_bfloat16*)dK;
-  p.part = (float*)((uint8_t*)workspace + rope::kStatusBytes);
+  p.part = q_weight ? (float*)((uint8_t*)workspace + rope::kStatusBytes) : nullptr;
   int grid = 0;
   if (T > 0) {
     grid = rope::bwd_grid(T, rope::passes_of(Hq, Hk, 1, d), num_sms(), p.parts);
