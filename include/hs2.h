@@ -457,6 +457,10 @@ HS2_API hs2_status hs2_page_table_update(int32_t* page_table, int B, int max_pag
  * out [B, 1, Hq, d] bf16; lse [B, 1, Hq] fp32 natural log, or NULL
  * The split of the work depends on the lengths and the call's sizes only, and partial results are joined in
  * a fixed order: results do not vary from run to run.
+ * The host chooses the form of the launch by B, Hk, window and max_pages (the lengths are on the device): a table no wider
+ * than short sequences need gets one launch, a wider one two (one sequence of 1,000 tokens: 2 to 3 us more). Probabilities
+ * are rounded to bf16 once; in the one-launch form, with at most 256 visible keys, to two bf16 terms; beside e4m3
+ * codes they are two e4m3 terms.
  * Supported: d = 128, or d = 64 with a bf16 cache; Hq / Hk <= 64; page_size % 16 == 0. Workspace:
  * hs2_paged_attn_workspace_bytes.
  */

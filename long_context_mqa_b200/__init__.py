@@ -717,8 +717,8 @@ def rope_frequencies(rot: int, base: float = 10000.0, *, scaling: str | None = N
       "ntk"     the base raised to base * factor^(rot / (rot - 2)): the slowest pair is interpolated by
                 `factor`, the fastest keeps its frequency
       "yarn"    by the turns r_i = original_len f_i / 2 pi that a pair makes over the original length: g f_i +
-                (1 - g) f_i / factor with g = (r_i - beta_slow) / (beta_fast - beta_slow) clamped to [0, 1], and
-                mscale = 0.1 ln(factor) + 1
+                (1 - g) f_i / factor with g = (r_i - beta_slow) / (beta_fast - beta_slow) clamped to [0, 1] (linear
+                in the turns, not in i), and mscale = 0.1 ln(factor) + 1
     """
     if rot < 2 or rot % 2 or not base > 0 or not factor >= 1:
         raise ValueError("rot must be even and positive, base positive, factor at least 1")

@@ -25,14 +25,17 @@
 // The tiles of all (sequence, key head) pairs form one line that is cut into ranges of equal cost, one per
 // CTA, from the lengths on the device (a captured launch serves any lengths). A pair that lies in one
 // CTA's range is finished there; the others leave (m, l, acc) records that a second kernel joins in
-// the order of the ranges, so results do not vary from run to run. Short sequences take clusters instead.
+// the order of the ranges, so results do not vary from run to run. Calls whose page table has room for short sequences
+// only take clusters instead (cluster_size).
 //
 // Measured against 6.56 TB/s, the memory's rate for a copy, in passes one after the other: 8 sequences of
 // 256k tokens, 64 heads on one key head, 171 us (6.3 TB/s; 183 us when a long run holds the clocks at the
-// power limit); 48 of up to 8k, 32 heads on 8 in pages of 16, 95 us (6.2); e4m3 codes, 8 of up to 256k, 70 us
-// (4.7; 84 us at the power limit). There the tensor cores are 60% busy (M = 64 runs at half their rate, and
+// power limit); 48 of up to 8k, 32 heads on 8 in pages of 16, 96 us (6.1; 99); e4m3 codes, 8 of up to 256k, 70 us
+// (4.7; 81 us at the power limit). There the tensor cores are 60% busy (M = 64 runs at half their rate, and
 // both operands have two terms), and the softmax warps' chain from scores to P is as long as a tile's
-// load. About 10 us of the long cases are start and end: the first tiles' way, the last tiles' chain, the join.
+// load. About 10 us of the long cases are start and end: the first tiles' way, the last tiles' chain, the join. Windows
+// of 128 keys of 64 sequences, 64 heads on 8 in pages of 16, take 22 us for 5 us of bytes: a pair's two or three tiles are
+// little but its start and end. The line's kernels spill 4 to 48 bytes a thread (168 registers, two CTAs an SM).
 // Tried and slower: eight softmax warps of half the columns with their maxima exchanged (140 us for 118 at
 // 8 x 256k of e4m3); a part of the exponentials on the FMA pipe (114 for 110); the products of a row kept
 // in tensor memory with the row rescaled when its maximum moves (bf16 1% faster at 16k, e4m3 3% slower, or
@@ -979,6 +982,8 @@ static cudaError_t launch_clusters(const CUtensorMap& tk, const CUtensorMap& tv,
 }
 
 // CTAs of a cluster for `pairs` (sequence, key head) of at most n tiles each; 0: the line of tiles.
+// n comes from the page table's width (and the window): the lengths are on the device, so short sequences in a table for
+// long ones take the line (one of 1,000 tokens 11.3 us instead of 8.9, in e4m3 12.2 instead of 9.0).
 // Clusters spare the records and the second kernel, about five tiles' time, but share a pair's tiles among 8
 // CTAs at most, and a ragged batch's short pairs leave theirs idle (three quarters of the line's share
 // is what a batch of mixed lengths has to gain by). Measured, clusters and line: 64 heads on one key head, one

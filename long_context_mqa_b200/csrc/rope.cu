@@ -20,9 +20,12 @@
 // by 0.06), while the token's first rows are on their way. Loads of several rows are issued before the
 // first is used. All arithmetic is in 32 bits, rounded once at the store.
 //
-// Measured against a copy's 6.56 TB/s: 32k tokens of 64 + 1 heads of 128, 185 us (5.9 TB/s; 200 us when a
-// long run holds the clocks at the power limit), their gradient 305 us (5.4; 320); 4,099 tokens of 32 + 8 heads
-// into e4m3 pages 20 us (4.6): one wave of warps, each waiting for six batches of rows in turn. Tried
+// Measured against a copy's 6.56 TB/s: 32k tokens of 64 + 1 heads of 128, 184 us (5.9 TB/s; 196 us when a
+// long run holds the clocks at the power limit), their gradient 298 us (5.5; 304); 4,099 tokens of 32 + 8 heads
+// into e4m3 pages 19.4 us (4.7): one wave of warps, each waiting for six batches of rows in turn. From 500 to 6,000 tokens a
+// warp has a few such batches and little else: 1,000 tokens 9.9 us for 5.1 us of bytes, 3,000 24.0 for 15.2; their
+// gradients, whose last passes run one at a time, 17.2 for 7.6 and 41.4 for 22.9. (Spills: up to 56 bytes a thread in the
+// forward's kernels, 32 in the gradient's.) Tried
 // and slower: rings in shared memory filled by cp.async for the gradient (368 us; it is the sums' chain that
 // waits), more and smaller batches at a higher occupancy (492), L2 prefetch of a warp's rows (211 for the
 // forward), streaming cache hints (no difference).
